@@ -403,6 +403,109 @@ bd_status bd_apply_multi_fp8(const uint8_t* w_codes, const float* w_scales, int6
                              int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------- */
+/* microscaled 4-bit matrices                                                          */
+/* ---------------------------------------------------------------------------------- */
+/* "BitDelta Guide", "3. Quantized Base Model Compatibility"; "Per-Axis Weight Deltas",
+ * Future Directions: INT4/FP8 co-design. A matrix X[rows][cols] is held as
+ *     X_hat[o][i] = row_scales[o] * s[o][i / B] * e2m1(codes[o][i]):
+ *   codes      : uint8 [rows][cols/2], two E2M1 codes per byte, the even column in the low
+ *                four bits. E2M1: bit 3 the sign, bits 0-2 the magnitudes 0, 0.5, 1, 1.5, 2,
+ *                3, 4, 6.
+ *   scales     : one byte per block of B columns of a row, in tiles of 128 rows x 4 blocks
+ *                (512 bytes, the order the tensor cores read): tile (R, C) starts at byte
+ *                (R * ceil(nb/4) + C) * 512 with nb = cols/B; row r and block c of a tile are
+ *                at (r % 32) * 16 + (r / 32) * 4 + c. Bytes of rows past `rows` and blocks past
+ *                nb must be zero. bd_fp4_scales_bytes() bytes; bd_prepare_fp4_scales writes
+ *                this layout from row-major scales.
+ *   row_scales : fp32 [rows], or NULL for all ones where a call only reads.
+ * Formats:
+ *   BD_FP4_NV  : B = 16, scales UE4M3 (E4M3 without a sign: the top bit must be 0; 0x7F is
+ *                NaN). bd_quantize_fp4 writes powers of two as row scales; a reader takes any
+ *                finite value (a checkpoint's one scale per tensor is that scale in every row).
+ *   BD_FP4_MX  : B = 32 (OCP MXFP4), scales E8M0 (2^(byte - 127); 0xFF is NaN).
+ * Shapes: 1 <= rows <= 2^24, 32 <= cols <= 2^24, cols % 32 == 0. */
+typedef enum { BD_FP4_NV = 0, BD_FP4_MX = 1 } bd_fp4_format;
+
+/* Bytes of the tiled block scales (0 for an invalid shape or format). */
+size_t bd_fp4_scales_bytes(int64_t rows, int64_t cols, int32_t fmt);
+
+/* bd_prepare_fp4_scales — row-major block scales uint8 [rows][cols/B] (as checkpoints hold
+ * them) -> the tiled layout, padding included. A re-ordering, no value changes. `out` must
+ * not overlap `scales` and is 16-byte aligned. */
+bd_status bd_prepare_fp4_scales(const uint8_t* scales, int32_t fmt, int64_t rows, int64_t cols,
+                                uint8_t* out, void* stream);
+
+/* bd_quantize_fp4 — quantises x (weights or activations) row by row.
+ *   BD_FP4_NV : row_scales[o] = 2^k with the least k in [-126, 126] for which
+ *               max_i |x[o][i]| <= 2688 * 2^k (2688 = 6 * 448; k = 0 for a row of zeros), and
+ *               with v = x / row_scales[o] a block's scale is E4M3(max|v| / 6), its codes
+ *               E2M1(v / scale): IEEE fp32 quotients, rounding to nearest even, magnitudes
+ *               above 6 saturating. A scale of 0 gives codes 0.
+ *   BD_FP4_MX : scale 2^e with e = floor(log2 max|block|) - 2 kept in [-127, 127] (-127 for a
+ *               block of zeros), codes E2M1(x / 2^e); row_scales may be NULL and is not written.
+ *   A block that holds an infinity or a NaN gets the NaN scale and codes 0: it reads as
+ *   NaN, in X_hat and in every product; other blocks are as if it were zero.
+ *   x         : [rows][cols], row stride ld >= cols elements (ld <= 2^31), BD_F32, BD_BF16 or
+ *               BD_F16; 16-byte aligned, and ld * element size a multiple of 16 when rows > 1.
+ *   codes, scales : fully overwritten, padding included; 16-byte aligned.
+ *   row_scales: 4-byte aligned.
+ *   x_hat     : optional (may be NULL) [rows][cols] of hat_dtype BD_F32 or BD_BF16: the
+ *               quantised values themselves, which both types hold exactly (down to their
+ *               subnormals), e.g. the base that bd_compress takes a fine-tune's delta against.
+ * Outputs must not overlap x. */
+bd_status bd_quantize_fp4(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ld,
+                          int32_t fmt, uint8_t* codes, uint8_t* scales, float* row_scales,
+                          void* x_hat, int32_t hat_dtype, void* stream);
+
+/* bd_dequantize_fp4 — out[rows][cols] = X_hat, BD_F32 (scale times code is exact, the row
+ * scale an fp32 product) or BD_BF16 (that value rounded to nearest even). */
+bd_status bd_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, const float* row_scales,
+                            int32_t fmt, int64_t rows, int64_t cols, void* out, int32_t out_dtype,
+                            void* stream);
+
+/* bd_matmul_fp4 — y[t] = W_hat x_hat[t]: both operands microscaled 4-bit in one format,
+ * multiplied as they are by the tensor cores' block-scaled kinds, fp32 accumulation; then
+ * the row scales of W and x.
+ *   w_*        : W [d_out][d_in];  x_* : tokens [tokens][d_in], 0 <= tokens <= 65536.
+ *   y          : [tokens][d_out], BD_BF16 (rounded to nearest even) or BD_F32.
+ *   workspace  : bd_matmul_fp4_workspace_size() bytes, 16-byte aligned. Only its status word is
+ *                used: this call sets BD_DEV_TIMEOUT in it and never clears it, so the caller
+ *                zeroes the workspace once before the first call.
+ * A NaN block makes NaN of every product with its row and of nothing else. tokens may be 0
+ * (nothing is launched). Results do not depend on timing. */
+size_t bd_matmul_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t tokens);
+bd_status bd_matmul_fp4(const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scales,
+                        const uint8_t* x_codes, const uint8_t* x_scales, const float* x_row_scales,
+                        int32_t fmt, int64_t d_out, int64_t d_in, int64_t tokens, void* y,
+                        int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* bd_linear_fp4 — y[t] = W_hat x[t] with bf16 activations x [tokens][d_in], 16-byte
+ * aligned. The tensor cores multiply 4-bit by 4-bit, so each block of x[t] is written as a
+ * sum of E2M1 limbs with power-of-two scales: 4 limbs for a BD_BF16 result, 6 for BD_F32.
+ * With m the block's largest magnitude, values from m/6 up (BD_BF16) or m/384 up (BD_F32) are
+ * exact and the others carry at most m * 2^-10 or m * 2^-16; what is smaller than 2^-17 of a
+ * token's largest magnitude may be lost in BD_FP4_NV (than 2^-126 in BD_FP4_MX). An infinity
+ * or a NaN in x[t] makes all of y[t] NaN.
+ *   workspace : bd_linear_fp4_workspace_size() bytes, 16-byte aligned; its status word is reset
+ *               by this call. tokens may be 0 (nothing is launched). */
+size_t bd_linear_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t tokens);
+bd_status bd_linear_fp4(const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scales,
+                        int32_t fmt, int64_t d_out, int64_t d_in, const void* x, int64_t tokens,
+                        void* y, int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* bd_apply_multi_fp4 — bd_apply_multi over a microscaled 4-bit base:
+ *     y[t] = W_hat x[t] + Delta_hat_{u(t)} x[t].
+ * Same tenants, ids, output and status rules as bd_apply_multi; x is bf16 [batch][d_in]; the
+ * base product is that of bd_linear_fp4 for the same y_dtype.
+ *   workspace : bd_apply_fp4_workspace_size() bytes, 16-byte aligned. */
+size_t bd_apply_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_tenants);
+bd_status bd_apply_multi_fp4(const uint8_t* w_codes, const uint8_t* w_scales,
+                             const float* w_row_scales, int32_t fmt, int64_t d_out, int64_t d_in,
+                             const bd_tenant* tenants, int32_t n_tenants, int32_t scale_dtype,
+                             const int32_t* tenant_ids, const void* x, int64_t batch, void* y,
+                             int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------- */
 /* status, diagnostics                                                                 */
 /* ---------------------------------------------------------------------------------- */
 /* Copies the device status word of a workspace (compress or apply) to *flags (host)

@@ -21,6 +21,8 @@ source pages state it:
 * ``oracle.fp8``: an e4m3 base with per-row scales under the same delta path ("BitDelta
   Guide", "3. Quantized Base Model Compatibility"; "Per-Axis Weight Deltas", Future
   Directions, FP8 co-design).
+* ``oracle.fp4``: microscaled 4-bit matrices (E2M1 codes, block scales in UE4M3 or E8M0)
+  and products of them (the same two sections).
 
 Every function here is pinned by ``tests/test_oracle.py`` against the pages' worked
 examples, closed forms, invariants or brute force; none is "parity unpinned".
@@ -53,4 +55,16 @@ from .fp8 import (  # noqa: F401
     quantize_base,
     dequantize_base,
     apply_multi_fp8,
+)
+from .fp4 import (  # noqa: F401
+    FP4_NV,
+    FP4_MX,
+    E2M1,
+    fp4_block,
+    e2m1_round,
+    e8m0_value,
+    quantize_fp4,
+    tile_scales,
+    dequantize_fp4,
+    apply_multi_fp4,
 )

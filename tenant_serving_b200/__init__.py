@@ -19,4 +19,8 @@ from ._lib import (  # noqa: F401
     bd_profile_collect, bd_selftest_wait_timeout, bd_tc_min_tokens,
     bd_cache_module, bd_cache_record_bytes, bd_prepare_record_host, CacheTable, TenantCache,
     bd_quantize_base_fp8, bd_apply_fp8_workspace_size, bd_apply_multi_fp8,
+    BD_FP4_NV, BD_FP4_MX, bd_fp4_scales_bytes, fp4_scales_shape, fp4_buffers, fp4_workspace,
+    bd_prepare_fp4_scales, bd_quantize_fp4, bd_dequantize_fp4, bd_matmul_fp4_workspace_size,
+    bd_matmul_fp4, bd_linear_fp4_workspace_size, bd_linear_fp4, bd_apply_fp4_workspace_size,
+    bd_apply_multi_fp4,
 )

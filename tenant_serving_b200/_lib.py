@@ -33,6 +33,7 @@ BD_F32, BD_BF16, BD_F16 = 0, 1, 2
 BD_SCALE_GROUP, BD_SCALE_ROW, BD_SCALE_COL, BD_SCALE_TENSOR, BD_SCALE_BLOCK = 0, 1, 2, 3, 4
 BD_DEV_TENANT_RANGE, BD_DEV_TIMEOUT, BD_DEV_TENANT_RECORD, BD_DEV_INTERNAL = 0x1, 0x2, 0x4, 0x8
 BD_LAYOUT_ROWMAJOR, BD_LAYOUT_TILED = 0, 1
+BD_FP4_NV, BD_FP4_MX = 0, 1
 
 EXPORTS = (
     "bd_compress", "bd_compress_noalloc", "bd_compress_workspace_size", "bd_reconstruct",
@@ -44,6 +45,9 @@ EXPORTS = (
     "bd_cache_table", "bd_cache_slots", "bd_cache_assign", "bd_cache_prefetch", "bd_cache_acquire",
     "bd_cache_release", "bd_cache_resident", "bd_quantize_base_fp8", "bd_apply_fp8_workspace_size",
     "bd_apply_multi_fp8",
+    "bd_fp4_scales_bytes", "bd_prepare_fp4_scales", "bd_quantize_fp4", "bd_dequantize_fp4",
+    "bd_matmul_fp4_workspace_size", "bd_matmul_fp4", "bd_linear_fp4_workspace_size", "bd_linear_fp4",
+    "bd_apply_fp4_workspace_size", "bd_apply_multi_fp4",
 )
 
 
@@ -161,6 +165,32 @@ def lib():
                                      c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_size_t,
                                      c_void_p]
     L.bd_apply_multi_fp8.restype = c_int32
+    L.bd_fp4_scales_bytes.argtypes = [c_int64, c_int64, c_int32]
+    L.bd_fp4_scales_bytes.restype = c_size_t
+    L.bd_prepare_fp4_scales.argtypes = [c_void_p, c_int32, c_int64, c_int64, c_void_p, c_void_p]
+    L.bd_prepare_fp4_scales.restype = c_int32
+    L.bd_quantize_fp4.argtypes = [c_void_p, c_int32, c_int64, c_int64, c_int64, c_int32, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_int32, c_void_p]
+    L.bd_quantize_fp4.restype = c_int32
+    L.bd_dequantize_fp4.argtypes = [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32,
+                                    c_void_p]
+    L.bd_dequantize_fp4.restype = c_int32
+    L.bd_matmul_fp4_workspace_size.argtypes = [c_int64, c_int64, c_int64]
+    L.bd_matmul_fp4_workspace_size.restype = c_size_t
+    L.bd_matmul_fp4.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64,
+                                c_int64, c_int64, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]
+    L.bd_matmul_fp4.restype = c_int32
+    L.bd_linear_fp4_workspace_size.argtypes = [c_int64, c_int64, c_int64]
+    L.bd_linear_fp4_workspace_size.restype = c_size_t
+    L.bd_linear_fp4.argtypes = [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int64,
+                                c_void_p, c_int32, c_void_p, c_size_t, c_void_p]
+    L.bd_linear_fp4.restype = c_int32
+    L.bd_apply_fp4_workspace_size.argtypes = [c_int64, c_int64, c_int64, c_int32]
+    L.bd_apply_fp4_workspace_size.restype = c_size_t
+    L.bd_apply_multi_fp4.argtypes = [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_void_p, c_int32,
+                                     c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_int32, c_void_p, c_size_t,
+                                     c_void_p]
+    L.bd_apply_multi_fp4.restype = c_int32
     _LIB = L
     return L
 
@@ -394,6 +424,215 @@ def bd_apply_multi_fp8(w_codes, w_scales, table, tenant_ids, x, y=None, y_dtype=
                                   table.scale_dtype, _ptr(tenant_ids), _ptr(x), batch, _ptr(y), dtype_code(y),
                                   _ptr(workspace), workspace.numel(), _stream(stream))
     check(rc, "bd_apply_multi_fp8")
+    return y, workspace
+
+
+class _here:
+    """Makes the device that holds all of a call's tensors the current one for the call (and
+    so its current stream the default); refuses tensors that live apart."""
+
+    def __init__(self, *ts):
+        torch = _torch()
+        ts = [t for t in ts if t is not None]
+        _require_cuda(*ts)
+        dev = ts[0].device
+        if any(t.device != dev for t in ts):
+            raise ValueError("the tensors of a call live on one GPU")
+        self._ctx = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def bd_fp4_scales_bytes(rows, cols, fmt) -> int:
+    return int(lib().bd_fp4_scales_bytes(int(rows), int(cols), int(fmt)))
+
+
+def fp4_scales_shape(rows, cols, fmt):
+    """(row tiles, block tiles, 512): the tiled block scales of a [rows, cols] matrix."""
+    rt = -(-int(rows) // 128)
+    return (rt, bd_fp4_scales_bytes(rows, cols, fmt) // (512 * rt), 512)
+
+
+def fp4_buffers(rows, cols, fmt, device):
+    """(codes, scales, row scales or None) to hold a [rows, cols] matrix in a 4-bit format."""
+    torch = _torch()
+    if bd_fp4_scales_bytes(rows, cols, fmt) == 0:
+        raise BitDeltaError(BD_ERR_SHAPE, "fp4_buffers")
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+    scales = torch.empty(fp4_scales_shape(rows, cols, fmt), dtype=torch.uint8, device=device)
+    row = torch.empty(rows, dtype=torch.float32, device=device) if fmt == BD_FP4_NV else None
+    return codes, scales, row
+
+
+def fp4_workspace(nbytes, device):
+    """A zeroed workspace (the 4-bit x 4-bit product keeps a status word in it)."""
+    torch = _torch()
+    return torch.zeros(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+def _fp4_shape(codes, scales, row_scales, fmt, where):
+    """[rows, cols] of a packed matrix, its buffers' sizes and types checked."""
+    torch = _torch()
+    rows, half = codes.shape
+    for t, dt in ((codes, torch.uint8), (scales, torch.uint8), (row_scales, torch.float32)):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"{where}: codes and scales are uint8, row scales float32")
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{where}: packed matrices are contiguous")
+    n = bd_fp4_scales_bytes(rows, 2 * half, fmt)
+    if n == 0 or scales.numel() != n or (row_scales is not None and row_scales.numel() != rows):
+        raise BitDeltaError(BD_ERR_SHAPE, where)
+    return rows, 2 * half
+
+
+def _fp4_out(y, shape, dtype, device, where):
+    torch = _torch()
+    if y is None:
+        return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
+    if tuple(y.shape) != tuple(shape) or not y.is_contiguous():
+        raise BitDeltaError(BD_ERR_SHAPE, where)
+    return y
+
+
+def bd_prepare_fp4_scales(scales, fmt, rows, cols, out=None, stream=None):
+    """Wrap ``bd_prepare_fp4_scales``: row-major block scales (uint8, or a float8 dtype of the
+    same bytes) -> the tiled layout."""
+    torch = _torch()
+    here = _here(scales, out)
+    shape = fp4_scales_shape(rows, cols, fmt) if bd_fp4_scales_bytes(rows, cols, fmt) else None
+    if shape is None or scales.element_size() != 1 or not scales.is_contiguous() or \
+            scales.numel() != rows * (cols // (16 if fmt == BD_FP4_NV else 32)):
+        raise BitDeltaError(BD_ERR_SHAPE, "bd_prepare_fp4_scales")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.uint8, device=scales.device)
+    elif out.numel() != bd_fp4_scales_bytes(rows, cols, fmt) or not out.is_contiguous():
+        raise BitDeltaError(BD_ERR_SHAPE, "bd_prepare_fp4_scales")
+    with here:
+        rc = lib().bd_prepare_fp4_scales(_ptr(scales), int(fmt), int(rows), int(cols), _ptr(out), _stream(stream))
+    check(rc, "bd_prepare_fp4_scales")
+    return out
+
+
+def bd_quantize_fp4(x, fmt, codes=None, scales=None, row_scales=None, hat=None, hat_dtype=None, stream=None):
+    """Wrap ``bd_quantize_fp4``: (codes uint8 [rows, cols/2], tiled scales uint8, row scales
+    fp32 [rows] or None for BD_FP4_MX, x_hat or None). ``x`` may have any row stride; x_hat is
+    written when ``hat`` or ``hat_dtype`` is given."""
+    torch = _torch()
+    here = _here(x, codes, scales, row_scales, hat)
+    rows, cols = x.shape
+    if x.stride(1) != 1 and cols > 1:
+        raise BitDeltaError(BD_ERR_SHAPE, "bd_quantize_fp4")
+    if codes is None or scales is None or (row_scales is None and fmt == BD_FP4_NV):
+        c, s, r = fp4_buffers(rows, cols, fmt, x.device)
+        codes, scales, row_scales = (codes if codes is not None else c), (scales if scales is not None else s), \
+            (row_scales if row_scales is not None else r)
+    if tuple(codes.shape) != (rows, cols // 2):
+        raise BitDeltaError(BD_ERR_SHAPE, "bd_quantize_fp4")
+    _fp4_shape(codes, scales, row_scales, fmt, "bd_quantize_fp4")
+    if hat is not None or hat_dtype is not None:
+        hat = _fp4_out(hat, (rows, cols), hat_dtype, x.device, "bd_quantize_fp4")
+    with here:
+        rc = lib().bd_quantize_fp4(_ptr(x), dtype_code(x), rows, cols, x.stride(0) if rows > 1 else cols, int(fmt),
+                                   _ptr(codes), _ptr(scales), _ptr(row_scales), _ptr(hat),
+                                   dtype_code(hat) if hat is not None else BD_F32, _stream(stream))
+    check(rc, "bd_quantize_fp4")
+    return codes, scales, row_scales, hat
+
+
+def bd_dequantize_fp4(codes, scales, row_scales, fmt, out=None, out_dtype=None, stream=None):
+    """Wrap ``bd_dequantize_fp4``: the values of a packed matrix, bf16 unless asked otherwise."""
+    here = _here(codes, scales, row_scales, out)
+    rows, cols = _fp4_shape(codes, scales, row_scales, fmt, "bd_dequantize_fp4")
+    out = _fp4_out(out, (rows, cols), out_dtype, codes.device, "bd_dequantize_fp4")
+    with here:
+        rc = lib().bd_dequantize_fp4(_ptr(codes), _ptr(scales), _ptr(row_scales), int(fmt), rows, cols, _ptr(out),
+                                     dtype_code(out), _stream(stream))
+    check(rc, "bd_dequantize_fp4")
+    return out
+
+
+def bd_matmul_fp4_workspace_size(d_out, d_in, tokens) -> int:
+    return int(lib().bd_matmul_fp4_workspace_size(int(d_out), int(d_in), int(tokens)))
+
+
+def bd_matmul_fp4(w_codes, w_scales, w_row, x_codes, x_scales, x_row, fmt, y=None, y_dtype=None, workspace=None,
+                  stream=None):
+    """Wrap ``bd_matmul_fp4``: (y [tokens, d_out], workspace) with y = X_hat W_hat^T. A workspace
+    of the caller's is zeroed once before its first use (``fp4_workspace``)."""
+    here = _here(w_codes, w_scales, w_row, x_codes, x_scales, x_row, y, workspace)
+    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, "bd_matmul_fp4")
+    tokens = x_codes.shape[0]
+    if tokens and _fp4_shape(x_codes, x_scales, x_row, fmt, "bd_matmul_fp4") != (tokens, d_in):
+        raise BitDeltaError(BD_ERR_SHAPE, "bd_matmul_fp4")
+    y = _fp4_out(y, (tokens, d_out), y_dtype, w_codes.device, "bd_matmul_fp4")
+    if workspace is None:
+        workspace = fp4_workspace(bd_matmul_fp4_workspace_size(d_out, d_in, tokens), w_codes.device)
+    with here:
+        rc = lib().bd_matmul_fp4(_ptr(w_codes), _ptr(w_scales), _ptr(w_row), _ptr(x_codes), _ptr(x_scales), _ptr(x_row),
+                                 int(fmt), d_out, d_in, tokens, _ptr(y), dtype_code(y), _ptr(workspace),
+                                 workspace.numel(), _stream(stream))
+    check(rc, "bd_matmul_fp4")
+    return y, workspace
+
+
+def bd_linear_fp4_workspace_size(d_out, d_in, tokens) -> int:
+    return int(lib().bd_linear_fp4_workspace_size(int(d_out), int(d_in), int(tokens)))
+
+
+def _bf16_rows(x, d_in, where):
+    torch = _torch()
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{where}: activations are bfloat16")
+    if x.dim() != 2 or x.shape[1] != d_in or not x.is_contiguous():
+        raise BitDeltaError(BD_ERR_SHAPE, where)
+    return x.shape[0]
+
+
+def bd_linear_fp4(w_codes, w_scales, w_row, x, fmt, y=None, y_dtype=None, workspace=None, stream=None):
+    """Wrap ``bd_linear_fp4``: (y [tokens, d_out], workspace) with y = x W_hat^T, x bf16."""
+    torch = _torch()
+    here = _here(w_codes, w_scales, w_row, x, y, workspace)
+    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, "bd_linear_fp4")
+    tokens = _bf16_rows(x, d_in, "bd_linear_fp4")
+    y = _fp4_out(y, (tokens, d_out), y_dtype, x.device, "bd_linear_fp4")
+    if workspace is None:
+        workspace = torch.empty(bd_linear_fp4_workspace_size(d_out, d_in, tokens), dtype=torch.uint8, device=x.device)
+    with here:
+        rc = lib().bd_linear_fp4(_ptr(w_codes), _ptr(w_scales), _ptr(w_row), int(fmt), d_out, d_in, _ptr(x), tokens,
+                                 _ptr(y), dtype_code(y), _ptr(workspace), workspace.numel(), _stream(stream))
+    check(rc, "bd_linear_fp4")
+    return y, workspace
+
+
+def bd_apply_fp4_workspace_size(d_out, d_in, batch, n_tenants) -> int:
+    return int(lib().bd_apply_fp4_workspace_size(int(d_out), int(d_in), int(batch), int(n_tenants)))
+
+
+def bd_apply_multi_fp4(w_codes, w_scales, w_row, table, tenant_ids, x, fmt, y=None, y_dtype=None, workspace=None,
+                       stream=None):
+    """Wrap ``bd_apply_multi_fp4``: y[t] = W_hat x[t] + Delta_hat_{ids[t]} x[t], W_hat a
+    microscaled 4-bit base."""
+    torch = _torch()
+    here = _here(w_codes, w_scales, w_row, table.dev, tenant_ids, x, y, workspace)
+    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, "bd_apply_multi_fp4")
+    batch = _bf16_rows(x, d_in, "bd_apply_multi_fp4")
+    if tenant_ids.dtype != torch.int32 or tenant_ids.numel() != batch:
+        raise BitDeltaError(BD_ERR_SHAPE, "bd_apply_multi_fp4")
+    y = _fp4_out(y, (batch, d_out), y_dtype, x.device, "bd_apply_multi_fp4")
+    if workspace is None:
+        workspace = torch.empty(max(bd_apply_fp4_workspace_size(d_out, d_in, batch, table.n), 16),
+                                dtype=torch.uint8, device=x.device)
+    with here:
+        rc = lib().bd_apply_multi_fp4(_ptr(w_codes), _ptr(w_scales), _ptr(w_row), int(fmt), d_out, d_in, table.ptr(),
+                                      table.n, table.scale_dtype, _ptr(tenant_ids), _ptr(x), batch, _ptr(y),
+                                      dtype_code(y), _ptr(workspace), workspace.numel(), _stream(stream))
+    check(rc, "bd_apply_multi_fp4")
     return y, workspace
 
 

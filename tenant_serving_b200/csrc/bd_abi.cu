@@ -1,4 +1,5 @@
 // Status strings, device status read-back, launch accounting and per-kernel timing.
+#include "bd_fp4.cuh"
 #include "bd_internal.cuh"
 #include "bd_tc.cuh"
 
@@ -8,16 +9,18 @@
 
 namespace bd {
 
-static const char* const kKernelNames[K_KIND_COUNT] = {
+static const char* const kKernelNames[kKindCount] = {
     "delta_stats",       "scale_signpack", "col_scale_signpack",
     "scale_final",       "reconstruct",  "tenant_bucket",  "base_gemv",
     "base_tc",           "delta_lut",    "prepare",
     "tc_gather",         "delta_tc",     "selftest_wait",
     "quant_fp8",         "x_limbs",      "base_fp8",
+    "fp4_quant",         "fp4_dequant",  "fp4_tile_scales",
+    "fp4_limbs",         "fp4_mm",
 };
 
 const char* kernel_name(int32_t kind) {
-  return (kind >= 0 && kind < K_KIND_COUNT) ? kKernelNames[kind] : "unknown";
+  return (kind >= 0 && kind < kKindCount) ? kKernelNames[kind] : "unknown";
 }
 
 namespace {
@@ -34,7 +37,7 @@ struct Profiler {
   std::vector<cudaEvent_t> pool;  // 2 per record
   std::vector<Rec> recs;
   size_t capacity = 0;
-  int64_t dropped[K_KIND_COUNT] = {0};
+  int64_t dropped[kKindCount] = {0};
   // pending begin event for the launch in progress (launch_begin / launch_end pair)
   int32_t open_kind = -1;
   cudaEvent_t open_e0 = nullptr;
@@ -62,7 +65,7 @@ void launch_begin(int32_t kind, cudaStream_t s) {
   std::lock_guard<std::mutex> lk(g_prof.mu);
   if (!g_prof.on) return;
   if (g_prof.recs.size() >= g_prof.capacity) {
-    if (kind >= 0 && kind < K_KIND_COUNT) g_prof.dropped[kind]++;
+    if (kind >= 0 && kind < kKindCount) g_prof.dropped[kind]++;
     g_prof.open_kind = -1;
     return;
   }
@@ -181,7 +184,7 @@ extern "C" bd_status bd_profile_enable(int32_t on, int32_t capacity) {
 
 extern "C" int32_t bd_profile_collect(int64_t* launches, double* total_ms, int32_t max_kinds) {
   std::lock_guard<std::mutex> lk(g_prof.mu);
-  const int n = max_kinds < K_KIND_COUNT ? max_kinds : K_KIND_COUNT;
+  const int n = max_kinds < kKindCount ? max_kinds : kKindCount;
   for (int k = 0; k < n; ++k) {
     if (launches) launches[k] = 0;
     if (total_ms) total_ms[k] = 0.0;

@@ -19,6 +19,7 @@
 //                    one pass over the tenant's bits.
 //   Both delta kernels add the base partial sums in a fixed order and write y (bf16 or
 //   fp32) in request order.
+#include "bd_fp4.cuh"
 #include "bd_internal.cuh"
 
 namespace bd {
@@ -299,16 +300,23 @@ struct ApplyLayout {
   int max_groups, max_tc;
   TcPlan tc;
   Fp8Plan f8;
+  Fp4Plan f4;
   int ksplit;
   int split_cap;  // lookup units (x K chunks) that may keep partial sums
   int64_t xg_rows;
-  size_t off_seg, off_tcrec, off_part, off_xg, off_xinv, off_x8, off_xmul, off_lpart, off_lcnt, total;
+  size_t off_seg, off_tcrec, off_part, off_xg, off_xinv, off_x8, off_x4s, off_xmul, off_lpart, off_lcnt, total;
 };
 
-// tc: the base product on the tensor cores (bf16 weights, or e4m3 ones when fp8)
+// What the base is held in. kBasePlain: w_dtype's own type; kBaseFp8: e4m3 codes; kBaseFp4 +
+// bd_fp4_format: microscaled 4-bit codes.
+constexpr int kBasePlain = 0, kBaseFp8 = 1, kBaseFp4 = 2;
+
+// tc: the base product on the tensor cores (bf16, e4m3 or 4-bit weights); limbs: the 4-bit
+// product's limbs per activation
 ApplyLayout layout_apply(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_tenants, bool tc,
-                         bool tc_delta, bool fp8 = false) {
-  ApplyLayout L;
+                         bool tc_delta, int base = kBasePlain, int limbs = 0) {
+  const bool fp8 = base == kBaseFp8, fp4 = base >= kBaseFp4;
+  ApplyLayout L = {};
   L.max_groups = max_groups_for(batch, n_tenants);
   if (L.max_groups < 1) L.max_groups = 1;
   // a batch smaller than the many-token threshold has no tensor-core segment at all
@@ -324,6 +332,8 @@ ApplyLayout layout_apply(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_t
   if (fp8) {
     L.f8 = plan_base_fp8(d_out, d_in, batch);
     L.ksplit = L.f8.ksplit;
+  } else if (fp4) {
+    if (batch > 0) L.f4 = plan_fp4(d_out, d_in, batch, limbs, base - kBaseFp4);
   } else if (tc) {
     L.tc = plan_base_tc(d_out, d_in, batch);
     L.ksplit = L.tc.ksplit;
@@ -340,9 +350,11 @@ ApplyLayout layout_apply(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_t
   L.off_xinv = off;
   off = align_up(off + (size_t)L.xg_rows * sizeof(float), 256);
   L.off_x8 = off;
-  off = align_up(off + (fp8 ? L.f8.x8_bytes : 0), 256);
+  off = align_up(off + (fp8 ? L.f8.x8_bytes : fp4 ? L.f4.xc_bytes : 0), 256);
+  L.off_x4s = off;
+  off = align_up(off + (fp4 ? L.f4.xs_bytes : 0), 256);
   L.off_xmul = off;
-  off = align_up(off + (fp8 ? (size_t)L.f8.xmul_count * sizeof(float) : 0), 256);
+  off = align_up(off + (fp8 ? (size_t)L.f8.xmul_count : fp4 ? (size_t)batch : 0) * sizeof(float), 256);
   // lookup-kernel K split: partial sums [unit][512 rows][4 tokens] and arrival counters
   {
     const int64_t tiles = (d_out + kLutTileRows - 1) / kLutTileRows;
@@ -370,32 +382,48 @@ size_t apply_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int32_t 
 
 size_t apply_fp8_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_tenants) {
   if (d_out < 1 || d_in < 32 || batch < 0 || n_tenants < 0) return 0;
-  return layout_apply(d_out, d_in, batch, n_tenants, true, (d_in % 64) == 0, true).total;
+  return layout_apply(d_out, d_in, batch, n_tenants, true, (d_in % 64) == 0, kBaseFp8).total;
 }
 
-// w_scales != nullptr: w_base holds e4m3 codes with per-row fp32 scales w_scales (x bf16)
+size_t apply_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_tenants) {
+  if (d_out < 1 || d_in < 32 || batch < 0 || n_tenants < 0) return 0;
+  size_t most = 0;
+  for (int fmt = BD_FP4_NV; fmt <= BD_FP4_MX; ++fmt)
+    for (int limbs : {kFp4LimbsBf16, kFp4LimbsF32}) {
+      const size_t n =
+          layout_apply(d_out, d_in, batch, n_tenants, true, (d_in % 64) == 0, kBaseFp4 + fmt, limbs).total;
+      if (n > most) most = n;
+    }
+  return most;
+}
+
+// base kBaseFp8: w_base holds e4m3 codes with per-row fp32 scales w_scales; base kBaseFp4 +
+// format: 4-bit codes, tiled block scales w_bscales, per-row scales w_scales or nullptr. x is
+// bf16 with both.
 bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t d_in,
                      const bd_tenant* tenants, int32_t n_tenants, int32_t scale_dtype,
                      const int32_t* tenant_ids, const void* x, int64_t batch, void* y,
                      int32_t y_dtype, void* workspace, size_t ws_bytes, cudaStream_t s,
-                     const float* w_scales = nullptr) {
-  const bool fp8 = w_scales != nullptr;
+                     int base = kBasePlain, const float* w_scales = nullptr,
+                     const uint8_t* w_bscales = nullptr) {
+  const bool fp8 = base == kBaseFp8, fp4 = base >= kBaseFp4;
   if (w_dtype != BD_BF16 && w_dtype != BD_F32) return BD_ERR_DTYPE;
   if (scale_dtype != BD_F16 && scale_dtype != BD_F32) return BD_ERR_DTYPE;
   if (y_dtype != BD_BF16 && y_dtype != BD_F32) return BD_ERR_DTYPE;
   if (d_out < 1 || d_in < 32 || (d_in % 32) != 0) return BD_ERR_SHAPE;
   if (batch < 0 || batch > kMaxBatch || n_tenants < 0 || n_tenants > kMaxTenants) return BD_ERR_SHAPE;
   if (batch == 0) return BD_OK;
-  if (!w_base || !x || !y || !tenant_ids) return BD_ERR_NULL;
+  if (!w_base || !x || !y || !tenant_ids || (fp4 && !w_bscales)) return BD_ERR_NULL;
   if (n_tenants > 0 && !tenants) return BD_ERR_NULL;
   if (!aligned16(w_base) || !aligned16(x) || !aligned16(y) || !aligned16(tenant_ids) ||
       (tenants && (reinterpret_cast<uintptr_t>(tenants) & 7u)) ||
-      (fp8 && (reinterpret_cast<uintptr_t>(w_scales) & 3u)))
+      ((fp8 || fp4) && (reinterpret_cast<uintptr_t>(w_scales) & 3u)) || (fp4 && !aligned16(w_bscales)))
     return BD_ERR_ALIGN;
-  const bool tc = w_dtype == BD_BF16;  // with an e4m3 base, w_dtype is the activations' bf16
+  const bool tc = w_dtype == BD_BF16;  // with an e4m3 or 4-bit base, w_dtype is the activations' bf16
   // the tensor-core delta path needs bf16 activations, fp16 scales and 64-column stages
   const bool tc_delta = tc && scale_dtype == BD_F16 && (d_in % 64) == 0;
-  ApplyLayout L = layout_apply(d_out, d_in, batch, n_tenants, tc, tc_delta, fp8);
+  ApplyLayout L = layout_apply(d_out, d_in, batch, n_tenants, tc, tc_delta, base,
+                               y_dtype == BD_F32 ? kFp4LimbsF32 : kFp4LimbsBf16);
   if (!workspace || ws_bytes < L.total) return BD_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BD_ERR_ALIGN;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -421,6 +449,15 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
   if (fp8) {
     bd_status st = launch_base_fp8(L.f8, static_cast<const uint8_t*>(w_base), w_scales, x, d_out, d_in, batch,
                                    ws + L.off_x8, reinterpret_cast<float*>(ws + L.off_xmul), y_part, status, s);
+    if (st != BD_OK) return st;
+  } else if (fp4) {
+    const int fmt = base - kBaseFp4;
+    uint8_t *xc = ws + L.off_x8, *xs = ws + L.off_x4s;
+    float* xmul = reinterpret_cast<float*>(ws + L.off_xmul);
+    bd_status st = launch_fp4_limbs(L.f4, fmt, x, d_in, batch, xc, xs, xmul, nullptr, s);
+    if (st != BD_OK) return st;
+    st = launch_fp4_mm(L.f4, fmt, Fp4Mat{static_cast<const uint8_t*>(w_base), w_bscales, w_scales},
+                       Fp4Mat{xc, xs, xmul}, d_out, d_in, batch, y_part, BD_F32, status, s);
     if (st != BD_OK) return st;
   } else if (tc) {
     bd_status st = launch_base_tc(L.tc, w_base, x, d_out, d_in, batch, y_part, status, s);
@@ -472,7 +509,23 @@ extern "C" bd_status bd_apply_multi_fp8(const uint8_t* w_codes, const float* w_s
                                         size_t ws_bytes, void* stream) {
   if (batch > 0 && !w_scales) return BD_ERR_NULL;  // (batch 0: shapes checked, nothing launched)
   return bd::apply_impl(w_codes, BD_BF16, d_out, d_in, tenants, n_tenants, scale_dtype, tenant_ids, x, batch, y,
-                        y_dtype, workspace, ws_bytes, static_cast<cudaStream_t>(stream), w_scales);
+                        y_dtype, workspace, ws_bytes, static_cast<cudaStream_t>(stream), bd::kBaseFp8, w_scales);
+}
+
+extern "C" size_t bd_apply_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_tenants) {
+  return bd::apply_fp4_workspace_size(d_out, d_in, batch, n_tenants);
+}
+
+extern "C" bd_status bd_apply_multi_fp4(const uint8_t* w_codes, const uint8_t* w_scales, const float* w_row_scales,
+                                        int32_t fmt, int64_t d_out, int64_t d_in, const bd_tenant* tenants,
+                                        int32_t n_tenants, int32_t scale_dtype, const int32_t* tenant_ids,
+                                        const void* x, int64_t batch, void* y, int32_t y_dtype, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  using namespace bd;
+  if (fmt != BD_FP4_NV && fmt != BD_FP4_MX) return BD_ERR_CONFIG;
+  if (d_out > kFp4MaxDim || d_in > kFp4MaxDim) return BD_ERR_SHAPE;
+  return apply_impl(w_codes, BD_BF16, d_out, d_in, tenants, n_tenants, scale_dtype, tenant_ids, x, batch, y, y_dtype,
+                    workspace, ws_bytes, static_cast<cudaStream_t>(stream), kBaseFp4 + fmt, w_row_scales, w_scales);
 }
 
 extern "C" bd_status bd_apply_multi(const void* w_base, int32_t w_dtype, int64_t d_out,
