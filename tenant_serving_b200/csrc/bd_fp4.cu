@@ -238,99 +238,119 @@ __global__ void __launch_bounds__(256) k_fp4_tile_scales(const uint8_t* __restri
 // largest block at s_0 = 2^8, and limbs below 2^-9 are dropped (an error of at most 2^-8,
 // below 2^-17 of the token's maximum, which is above 3 * 2^8). MX scales hold every power used, and k_t = 0.
 // ------------------------------------------------------------------------------------
-template <int FMT>
-__global__ void __launch_bounds__(128) k_fp4_limbs(const uint16_t* __restrict__ x, int64_t d_in, int limbs, int h,
-                                                   int n_stride, uint8_t* __restrict__ xc, uint8_t* __restrict__ xs,
-                                                   float* __restrict__ xmul, uint32_t* __restrict__ reset_status) {
+// One CTA per (token, 4096 columns), one thread per 16 columns; in NV every CTA of a token
+// takes the maximum of the whole row (a few loads per thread, all in flight).
+constexpr int kLimbThreads = 256;
+constexpr int kLimbChunk = kLimbThreads * 16;
+
+__device__ __forceinline__ uint32_t finite_max16(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t a = abs_bits(v[j]);
+    if (a < kInfBits) m = max(m, a);
+  }
+  return m;
+}
+
+template <int FMT, int L>
+__global__ void __launch_bounds__(kLimbThreads) k_fp4_limbs(const uint16_t* __restrict__ x, int64_t d_in, int h,
+                                                            int n_stride, uint8_t* __restrict__ xc,
+                                                            uint8_t* __restrict__ xs, float* __restrict__ xmul,
+                                                            uint32_t* __restrict__ reset_status) {
   pdl_wait();  // inputs may come from the previous kernel on the stream
   pdl_trigger();
-  __shared__ uint32_t red[4];
-  const int t = blockIdx.x;
-  if (reset_status && t == 0 && threadIdx.x == 0) *reset_status = 0;  // the status word reports this call
-  const int64_t tiles_k = fp4_tiles_k(d_in, FMT);
   constexpr int kBlock = fp4_block(FMT);
-  const uint16_t* xr = x + (int64_t)t * d_in;
-  const int64_t row0 = (int64_t)(t / h) * n_stride + t % h;
-  // the token's exponent: its largest finite |x| <= 6 * 2^8 * 2^k (1536 = 1.5 * 2^10)
   constexpr int kLow = FMT == BD_FP4_NV ? -9 : -127;  // lowest scale
-  uint32_t m = 0;
-  for (int64_t c = (int64_t)threadIdx.x * 16; FMT == BD_FP4_NV && c < d_in; c += 128 * 16) {
-    float v[16];
-    load16<BD_BF16>(xr, c, v);
+  __shared__ uint32_t red[kLimbThreads / 32];
+  const int t = blockIdx.x;
+  if (reset_status && t == 0 && blockIdx.y == 0 && threadIdx.x == 0) *reset_status = 0;  // reports this call
+  const int64_t tiles_k = fp4_tiles_k(d_in, FMT);
+  const uint16_t* xr = x + (int64_t)t * d_in;
+  const int64_t row0 = (int64_t)(t / h) * n_stride + (t % h) / 8 * (8 * L) + t % 8;
+  const int64_t c = (int64_t)blockIdx.y * kLimbChunk + threadIdx.x * 16;
+  const bool in = c < d_in;
+  float v[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t a = abs_bits(v[j]);
-      if (a < kInfBits) m = max(m, a);
-    }
-  }
-  if (FMT == BD_FP4_NV) m = block_umax(m, red);
+  for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  if (in) load16<BD_BF16>(xr, c, v);
   int k = 0;
-  if (m > 0) {
-    k = (int)(m >> 23) - 127 - 10 + ((m & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    k = k < -126 ? -126 : k;
-  }
-  if (threadIdx.x == 0) xmul[t] = pow2f(k);
-  const float down = pow2f(-k);
-  const int64_t nb = d_in / kBlock;
-  for (int l = 0; l < limbs; ++l) {
-    uint8_t* sr = xs + fp4_scale_row(row0 + (int64_t)l * h, tiles_k);
-    for (int64_t b = nb + threadIdx.x; b < 4 * tiles_k; b += 128) sr[(b >> 2) * kFp4TileBytes + (b & 3)] = 0;
-  }
-  for (int64_t c0 = (int64_t)(threadIdx.x & ~31) * 16; c0 < d_in; c0 += 128 * 16) {
-    const int64_t c = c0 + (threadIdx.x & 31) * 16;
-    const bool in = c < d_in;
-    float v[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = 0.f;
-    if (in) load16<BD_BF16>(xr, c, v);
-    uint32_t bm = 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) bm = max(bm, abs_bits(v[j]));
-    if (FMT == BD_FP4_MX) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-    const bool bad = bm >= kInfBits;
-    // s_0 = 2^e: least e with max|v| <= 6 * 2^e = 1.5 * 2^(e + 2)
-    const uint32_t am = bad ? 0u : abs_bits(__uint_as_float(bm) * down);
-    int e = (int)(am >> 23) - 127 - 2 + ((am & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    if (e < kLow) e = kLow;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] *= down;
-    for (int l = 0; l < limbs; ++l) {
-      const int el = e - (l == 0 ? 0 : 3 * l - 1);
-      const bool live = !bad && el >= kLow;
-      float q[16];
-      const float up = pow2f(live ? -el : 0), s = live ? pow2f(el) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) q[j] = live ? v[j] * up : 0.f;
-      __half2 hh[8];
-      const uint2 p = make_uint2(e2m1_round8(q, hh), e2m1_round8(q + 8, hh + 4));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {  // the remainder is exact: a multiple of v's lowest bit
-        const float2 f = __half22float2(hh[j]);
-        v[2 * j] = fmaf(-f.x, s, v[2 * j]);
-        v[2 * j + 1] = fmaf(-f.y, s, v[2 * j + 1]);
+  if (FMT == BD_FP4_NV) {
+    // the token's exponent: its largest finite |x| <= 6 * 2^8 * 2^k (1536 = 1.5 * 2^10)
+    uint32_t m = finite_max16(v);
+#pragma unroll 4
+    for (int64_t o = threadIdx.x * 16; o < d_in; o += kLimbChunk)
+      if (o != c) {
+        float u[16];
+        load16<BD_BF16>(xr, o, u);
+        m = max(m, finite_max16(u));
       }
-      if (in) {
-        const int64_t row = row0 + (int64_t)l * h;
-        *reinterpret_cast<uint2*>(xc + row * (d_in >> 1) + (c >> 1)) = p;
-        const int64_t b = c / kBlock;
-        uint32_t code;
-        if (FMT == BD_FP4_NV)  // E4M3: 2^el is a normal code from 2^-6 on, then 4, 2, 1
-          code = bad ? 0x7Fu : (!live ? 0u : (el >= -6 ? (uint32_t)(el + 7) << 3 : 1u << (el + 9)));
-        else
-          code = bad ? 0xFFu : (!live ? 0u : (uint32_t)(el + 127));
-        if (FMT == BD_FP4_NV || (threadIdx.x & 1) == 0)
-          xs[fp4_scale_row(row, tiles_k) + (b >> 2) * kFp4TileBytes + (b & 3)] = (uint8_t)code;
-      }
+    m = block_umax(m, red);
+    if (m > 0) {
+      k = (int)(m >> 23) - 127 - 10 + ((m & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+      k = k < -126 ? -126 : k;
     }
+  }
+  if (threadIdx.x == 0 && blockIdx.y == 0) xmul[t] = pow2f(k);
+  // padding scales past the row's last block are zero: at most 3 of them
+  const int64_t nb = d_in / kBlock;
+  if (blockIdx.y == 0 && threadIdx.x < 4 * L) {
+    const int64_t b = nb + threadIdx.x / L;
+    if (b < 4 * tiles_k)
+      xs[fp4_scale_row(row0 + (threadIdx.x % L) * 8, tiles_k) + (b >> 2) * kFp4TileBytes + (b & 3)] = 0;
+  }
+  uint32_t bm = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) bm = max(bm, abs_bits(v[j]));
+  if (FMT == BD_FP4_MX) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+  if (!in) return;  // (two threads of an MX block go together)
+  const bool bad = bm >= kInfBits;
+  const float down = pow2f(-k);
+  // s_0 = 2^e: least e with max|v| <= 6 * 2^e = 1.5 * 2^(e + 2)
+  const uint32_t am = bad ? 0u : abs_bits(__uint_as_float(bm) * down);
+  int e = (int)(am >> 23) - 127 - 2 + ((am & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+  if (e < kLow) e = kLow;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = bad ? 0.f : v[j] * down;
+  const int64_t b = c / kBlock;
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    const int el = e - (l == 0 ? 0 : 3 * l - 1);
+    const bool live = el >= kLow;
+    const float up = live ? pow2f(-el) : 0.f, s = live ? pow2f(el) : 0.f;
+    float q[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) q[j] = v[j] * up;
+    __half2 hh[8];
+    const uint2 p = make_uint2(e2m1_round8(q, hh), e2m1_round8(q + 8, hh + 4));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // the remainder is exact: a multiple of v's lowest bit
+      const float2 f = __half22float2(hh[j]);
+      v[2 * j] = fmaf(-f.x, s, v[2 * j]);
+      v[2 * j + 1] = fmaf(-f.y, s, v[2 * j + 1]);
+    }
+    const int64_t row = row0 + 8 * l;
+    *reinterpret_cast<uint2*>(xc + row * (d_in >> 1) + (c >> 1)) = p;
+    uint32_t code;
+    if (FMT == BD_FP4_NV)  // E4M3: 2^el is a normal code from 2^-6 on, then 4, 2, 1
+      code = bad ? 0x7Fu : (!live ? 0u : (el >= -6 ? (uint32_t)(el + 7) << 3 : 1u << (el + 9)));
+    else
+      code = bad ? 0xFFu : (!live ? 0u : (uint32_t)(el + 127));
+    if (FMT == BD_FP4_NV || (threadIdx.x & 1) == 0)
+      xs[fp4_scale_row(row, tiles_k) + (b >> 2) * kFp4TileBytes + (b & 3)] = (uint8_t)code;
   }
 }
 
 bd_status launch_fp4_limbs(const Fp4Plan& p, int fmt, const void* x, int64_t d_in, int64_t tokens, uint8_t* xc,
                            uint8_t* xs, float* xmul, uint32_t* reset_status, cudaStream_t s) {
+  auto* fn = fmt == BD_FP4_NV ? (p.limbs == kFp4LimbsBf16 ? k_fp4_limbs<BD_FP4_NV, kFp4LimbsBf16>
+                                                          : k_fp4_limbs<BD_FP4_NV, kFp4LimbsF32>)
+                              : (p.limbs == kFp4LimbsBf16 ? k_fp4_limbs<BD_FP4_MX, kFp4LimbsBf16>
+                                                          : k_fp4_limbs<BD_FP4_MX, kFp4LimbsF32>);
+  const int64_t chunks = (d_in + kLimbChunk - 1) / kLimbChunk;  // at most 4096
   launch_begin(K_FP4_LIMBS, s);
-  auto* fn = fmt == BD_FP4_NV ? k_fp4_limbs<BD_FP4_NV> : k_fp4_limbs<BD_FP4_MX>;
-  BD_CUDA_TRY(launch_pdl(fn, dim3((unsigned)tokens), dim3(128), 0, s, static_cast<const uint16_t*>(x), d_in, p.limbs,
-                         p.h, p.n_stride, xc, xs, xmul, reset_status));
+  BD_CUDA_TRY(launch_pdl(fn, dim3((unsigned)tokens, (unsigned)chunks), dim3(kLimbThreads), 0, s,
+                         static_cast<const uint16_t*>(x), d_in, p.h, p.n_stride, xc, xs, xmul, reset_status));
   launch_end(K_FP4_LIMBS, s);
   BD_LAUNCH_CHECK();
   return BD_OK;

@@ -107,12 +107,15 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t code) {
   return code == 0xFFu ? __uint_as_float(0x7FFFFFFFu) : pow2f((int)code - 127);
 }
 
-// Launch plan of a 4-bit product D[W rows][X rows]: X rows are tokens, or `limbs` rows per
-// token (N tile j then holds h tokens as rows j * n_stride + limb * h + token).
+// Launch plan of a 4-bit product D[W rows][X rows]. X rows are tokens, or `limbs` rows per
+// token: N tile j holds h tokens from row j * n_stride, limb l of its token t in row
+// (t / 8) * 8 * limbs + 8 * l + t % 8.
 struct Fp4Plan {
+  int pair;                     // the kernel for many X rows
   int limbs, h;                 // limb rows per token; tokens of an N tile
   int n_tile, n_stride;         // X rows of a tile (MMA N), distance of the tiles' first rows
   int tiles_n, tiles_m, kblocks, split, stages;
+  int64_t ctas;
   size_t smem;
   int64_t x_rows;               // rows of the X operand (limb rows padded to whole tiles)
   size_t xc_bytes, xs_bytes;    // limb codes and scales in the workspace (0 without limbs)

@@ -2,13 +2,19 @@
 // tcgen05.mma kind::mxf4nvf4 (block 16, UE4M3 scales) or kind::mxf4 (block 32, E8M0 scales),
 // fp32 accumulation in tensor memory.
 //
-// One CTA owns a 128-row block of W and n_tile rows of X and a range of K; the CTAs of a
-// cluster split K. Warp 0 issues the loads of a 256-column stage (codes by TMA with the
-// 128-byte swizzle, their block scales by plain bulk copies: the tiled layout keeps a
-// stage's scales of 128 rows contiguous), warp 1 copies the scales to tensor memory
-// (tcgen05.cp) and issues the four K = 64 MMAs. The epilogue adds the limbs of a token; with
-// a split, each CTA leaves its fp32 sums in its own shared memory and the CTAs of the cluster
-// add them in rank order over distributed shared memory, so results do not depend on timing.
+// Two kernels:
+//   k_fp4_mm_rows  few X rows (one N tile of at most 256): bound by reading W. One CTA per
+//                  (128-row block of W, N tile, K range); the CTAs of a cluster split K and
+//                  add their fp32 sums in rank order in distributed shared memory.
+//   k_fp4_mm_pair  many X rows: bound by the tensor cores. Persistent CTA pairs
+//                  (cta_group::2), a 256 x 256 tile each.
+// In both, warp 0 issues the loads of 256-column stages (codes with the 128-byte swizzle, and
+// their block scales, which the tiled layout keeps contiguous) and warp 1 copies the scales to
+// tensor memory (tcgen05.cp) and issues the four K = 64 MMAs of a stage. No sum depends on
+// timing.
+//
+// X rows are tokens, or limbs of tokens in groups of 8: rows 8 L g + 8 l + j of a tile are
+// limb l of its token 8 g + j, so a group's sums are 8 L neighbouring accumulator columns.
 #include "bd_fp4.cuh"
 #include "bd_tc.cuh"
 
@@ -65,32 +71,90 @@ __host__ __device__ constexpr uint32_t umma_idesc_fp4(int m, int n, bool e8m0, i
          | ((uint32_t)sf_id << 29);       // A scale id
 }
 
-// 32 lanes x 8 consecutive 32-bit columns of tensor memory
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
-  uint32_t u[8];
+// One lane of a converged warp, the same one each time. Operands of the tensor-core and copy
+// instructions live in uniform registers; behind a `lane == 0` branch the compiler cannot
+// know that they are, and moves each operand there lane by lane (73 cycles per instruction
+// measured, 1170 for the sixteen of a stage).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = __uint_as_float(u[j]);
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t map_cluster(uint32_t saddr, uint32_t rank) {
   uint32_t a;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+  return a;
+}
+
+// N (8, 16 or 32) consecutive 32-bit columns of the thread's lane; tmem_wait() before use
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t* r) {
+  static_assert(N == 8 || N == 16 || N == 32, "");
+  if (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  else if (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Accumulator columns come in groups that hold whole tokens: 32 tokens without limbs, else
+// the 8 L columns of 8 tokens.
+template <int L>
+struct Group {
+  static constexpr int kCols = L == 1 ? 32 : 8 * L;
+  static constexpr int kTok = kCols / L;
+};
+// sums of a group's tokens, the smallest limb first
+template <int L>
+__device__ __forceinline__ void load_group(uint32_t taddr, float* v) {
+  uint32_t r[Group<L>::kCols];
+  tmem_load<32>(taddr, r);
+  if (L == 6) tmem_load<16>(taddr + 32, r + 32);
+  tmem_wait();
+#pragma unroll
+  for (int j = 0; j < Group<L>::kTok; ++j) {
+    float a = __uint_as_float(r[8 * (L - 1) + j]);
+#pragma unroll
+    for (int l = L - 2; l >= 0; --l) a += __uint_as_float(r[8 * l + j]);
+    v[j] = a;
+  }
 }
 
 struct MmArgs {
@@ -99,39 +163,54 @@ struct MmArgs {
   void* y;
   uint32_t* status;
   int64_t d_out, tokens;
-  int tiles_kw;                        // scale tiles along K
-  int limbs, h, n_tile, n_stride, kblocks, k_steps, split, stages, y_bf16;
-  int x_row_tiles;                     // scale tiles along the rows of X
+  int tiles_kw;     // scale tiles along K
+  int x_row_tiles;  // scale tiles along the rows of X
+  int h, n_tile, n_stride, tiles_n, kblocks, k_steps, split, stages, y_bf16;
+  int w_early;      // nothing still running on the stream writes W or its scales
+  int y_tma;        // y's rows are whole 16-byte units: tiles go out through tm_y
 };
 
-template <int FMT>
-__global__ void __launch_bounds__(kMmThreads) k_fp4_mm(const __grid_constant__ CUtensorMap tm_w,
-                                                       const __grid_constant__ CUtensorMap tm_x, const MmArgs p) {
+__device__ __forceinline__ void store_y(const MmArgs& p, int64_t t, int64_t row, float v) {
+  if (p.y_bf16)
+    reinterpret_cast<uint16_t*>(p.y)[t * p.d_out + row] = (uint16_t)f2bf_bits(v);
+  else
+    reinterpret_cast<float*>(p.y)[t * p.d_out + row] = v;
+}
+
+// ------------------------------------------------------------------------------------
+// few X rows
+// ------------------------------------------------------------------------------------
+template <int FMT, int L>
+__global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constant__ CUtensorMap tm_w,
+                                                            const __grid_constant__ CUtensorMap tm_x,
+                                                            const MmArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kTilesPerStage = FMT == BD_FP4_NV ? 4 : 2;   // scale tiles of a stage, per 128 rows
   constexpr uint32_t kSfBytes = kTilesPerStage * kFp4TileBytes;
   const int sfb_tiles = (p.n_tile + 127) / 128;              // 128-row scale tiles of the X rows
   const uint32_t b_bytes = (uint32_t)p.n_tile * 128u;
-  const int stages = p.stages;
+  const int stages = p.stages, split = p.split;
   uint8_t* sa = smem;
   uint8_t* sb = sa + (size_t)stages * kMmABytes;
   uint8_t* ssa = sb + (size_t)stages * b_bytes;
   uint8_t* ssb = ssa + (size_t)stages * kSfBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ssb + (size_t)stages * sfb_tiles * kSfBytes);
+  // with a split: this CTA's share of the tile's sums from every CTA, [rank][share][128 rows]
+  float* gather = reinterpret_cast<float*>(ssb + (size_t)stages * sfb_tiles * kSfBytes);
+  const int share = split > 1 ? (p.h + split - 1) / split : 0;  // tokens of a CTA
+  float* xr = gather + (size_t)split * share * 128;             // the tile's token scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(xr + p.h);
   uint64_t* empty = full + stages;
   uint64_t* done = empty + stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* issued_out = reinterpret_cast<int*>(tmem_slot + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = p.split;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
   const int64_t item = blockIdx.x / split;
-  const int tiles_n = (int)((p.tokens + p.h - 1) / p.h);
-  const int n_blk = (int)(item % tiles_n);
-  const int64_t m_blk = item / tiles_n;
+  const int n_blk = (int)(item % p.tiles_n);
+  const int64_t m_blk = item / p.tiles_n;
   const int kb0 = (int)((int64_t)p.kblocks * rank / split), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
   const int nkb = kb1 - kb0;  // >= 1: split <= kblocks
 
@@ -142,6 +221,7 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm(const __grid_constant__ C
   uint32_t tcols = 32;
   while (tcols < d_cols + 2 * sf_cols) tcols <<= 1;
 
+  if (split > 1) cluster_arrive();  // this CTA has started
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
@@ -159,14 +239,35 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm(const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_d = *tmem_slot;
-  pdl_wait();  // the set-up above overlaps the previous kernel on the stream
-  pdl_trigger();
 
   bool timed_out = false;
   if (warp == 0) {
-    if (lane == 0) {
-      int issued = 0;
       const int64_t x_row0 = (int64_t)n_blk * p.n_stride;
+      const int xt0 = (int)(x_row0 >> 7);
+      const int xt = min(sfb_tiles, p.x_row_tiles - xt0);
+      auto sf_of = [&](int i) {
+        return (uint32_t)min(kTilesPerStage, p.tiles_kw - (kb0 + i) * kTilesPerStage) * kFp4TileBytes;
+      };
+      auto load_w = [&](int i) {
+        const int s = i % stages;
+        const uint32_t sf = sf_of(i);
+        mbar_arrive_expect_tx(&full[s], kMmABytes + b_bytes + sf * (1 + xt));
+        tma_load_2d(sa + (size_t)s * kMmABytes, &tm_w, &full[s], (kb0 + i) * 128, (int)(m_blk * 128));
+        bulk_load(ssa + (size_t)s * kSfBytes,
+                  p.w_scales + (m_blk * p.tiles_kw + (int64_t)(kb0 + i) * kTilesPerStage) * kFp4TileBytes, sf, &full[s]);
+      };
+      // the weights of the first stages are asked for before the kernel that writes X is over
+      const int first = min(nkb, stages);
+      int early = 0;
+      if (p.w_early) {
+        if (elect_one())
+          for (int i = 0; i < first; ++i) load_w(i);
+        __syncwarp();
+        early = first;
+      }
+      pdl_wait();
+      pdl_trigger();
+      int issued = 0;
       for (int i = 0; i < nkb; ++i) {
         const int s = i % stages;
         const uint32_t ph = (uint32_t)(i / stages) & 1u;
@@ -175,62 +276,73 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm(const __grid_constant__ C
           *abort_flag = 1;
           break;
         }
-        const int kb = kb0 + i;
-        const int t0 = kb * kTilesPerStage;
-        const uint32_t sf = (uint32_t)min(kTilesPerStage, p.tiles_kw - t0) * kFp4TileBytes;
-        const int xt0 = (int)(x_row0 >> 7);
-        const int xt = min(sfb_tiles, p.x_row_tiles - xt0);
-        mbar_arrive_expect_tx(&full[s], kMmABytes + b_bytes + sf * (1 + xt));
-        tma_load_2d(sa + (size_t)s * kMmABytes, &tm_w, &full[s], kb * 128, (int)(m_blk * 128));
-        bulk_load(ssa + (size_t)s * kSfBytes, p.w_scales + ((int64_t)m_blk * p.tiles_kw + t0) * kFp4TileBytes, sf,
-                  &full[s]);
-        tma_load_2d(sb + (size_t)s * b_bytes, &tm_x, &full[s], kb * 128, (int)x_row0);
-        for (int j = 0; j < xt; ++j)
-          bulk_load(ssb + ((size_t)s * sfb_tiles + j) * kSfBytes,
-                    p.x_scales + ((int64_t)(xt0 + j) * p.tiles_kw + t0) * kFp4TileBytes, sf, &full[s]);
+        if (elect_one()) {
+          if (i >= early) load_w(i);
+          const uint32_t sf = sf_of(i);
+          tma_load_2d(sb + (size_t)s * b_bytes, &tm_x, &full[s], (kb0 + i) * 128, (int)x_row0);
+          for (int j = 0; j < xt; ++j)
+            bulk_load(
+                ssb + ((size_t)s * sfb_tiles + j) * kSfBytes,
+                p.x_scales + ((int64_t)(xt0 + j) * p.tiles_kw + (int64_t)(kb0 + i) * kTilesPerStage) * kFp4TileBytes,
+                sf, &full[s]);
+        }
+        __syncwarp();
         ++issued;
       }
-      *issued_out = issued;
-    }
-    __syncwarp();
+      if (lane == 0) *issued_out = issued;
   } else if (warp == 1) {
-    if (lane == 0) {
+      // Everything that a stage needs is a constant step from the stage before: the issuing
+      // thread has 512 cycles of MMAs per stage to hide its own work behind.
       const uint32_t id0 = umma_idesc_fp4(128, p.n_tile, FMT == BD_FP4_MX, 0);
       const uint32_t id1 = umma_idesc_fp4(128, p.n_tile, FMT == BD_FP4_MX, 2);
+      const uint64_t ad0 = umma_desc_sw128(smem_u32(sa)), bd0 = umma_desc_sw128(smem_u32(sb));
+      const uint64_t sad0 = scale_desc(smem_u32(ssa)), sbd0 = scale_desc(smem_u32(ssb));
+      const uint32_t b_step = b_bytes >> 4, sb_step = (uint32_t)sfb_tiles * (kSfBytes >> 4);
+      const bool two = sfb_tiles == 2;
+      int s = 0;
+      uint32_t ph = 0;
       for (int i = 0; i < nkb; ++i) {
-        const int s = i % stages;
-        const uint32_t ph = (uint32_t)(i / stages) & 1u;
         if (!mbar_wait(&full[s], ph, abort_flag)) {
           timed_out = true;
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
-        // scales: SFA tile of a step in 4 columns, SFB likewise per 128 rows, steps apart
-        const uint32_t sfa = tmem_d + d_cols + (uint32_t)(i & 1) * sf_cols;
-        const uint32_t sfb = sfa + kSfaCols;
-        const int steps = min(4, p.k_steps - (kb0 + i) * 4);
-        const int sf_tiles = FMT == BD_FP4_NV ? steps : (steps + 1) / 2;
-        for (int t = 0; t < sf_tiles; ++t) {
-          tmem_cp_scales(sfa + 4 * t, scale_desc(smem_u32(ssa + (size_t)s * kSfBytes + t * kFp4TileBytes)));
-          for (int j = 0; j < sfb_tiles; ++j)
-            tmem_cp_scales(sfb + 4 * (t * sfb_tiles + j),
-                           scale_desc(smem_u32(ssb + ((size_t)s * sfb_tiles + j) * kSfBytes + t * kFp4TileBytes)));
+        if (elect_one()) {
+          const uint32_t sfa = tmem_d + d_cols + (uint32_t)(i & 1) * sf_cols;
+          const uint32_t sfb = sfa + kSfaCols;
+          const uint64_t ad = ad0 + (uint32_t)s * (kMmABytes >> 4), bdsc = bd0 + (uint32_t)s * b_step;
+          const uint64_t sad = sad0 + (uint32_t)s * (kSfBytes >> 4), sbd = sbd0 + (uint32_t)s * sb_step;
+          const int steps = p.k_steps - (kb0 + i) * 4;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) {
+              // scales: SFA tile of a step in 4 columns, SFB likewise per 128 rows
+              const int t = FMT == BD_FP4_NV ? k : k >> 1;
+              const uint32_t sfb_t = sfb + (two ? 8 : 4) * t;
+              if (FMT == BD_FP4_NV || (k & 1) == 0) {
+                tmem_cp_scales(sfa + 4 * t, sad + t * (kFp4TileBytes >> 4));
+                tmem_cp_scales(sfb_t, sbd + t * (kFp4TileBytes >> 4));
+                if (two) tmem_cp_scales(sfb_t + 4, sbd + (kSfBytes >> 4) + t * (kFp4TileBytes >> 4));
+              }
+              // 64 columns: 32 bytes further inside the swizzled 128-byte row
+              umma_fp4<FMT>(tmem_d, ad + 2 * k, bdsc + 2 * k, FMT == BD_FP4_MX && (k & 1) ? id1 : id0, sfa + 4 * t,
+                            sfb_t, k > 0 ? 1u : (i > 0 ? 1u : 0u));
+            }
+          umma_commit(&empty[s]);
         }
-        const uint64_t ad = umma_desc_sw128(smem_u32(sa + (size_t)s * kMmABytes));
-        const uint64_t bdsc = umma_desc_sw128(smem_u32(sb + (size_t)s * b_bytes));
-        for (int k = 0; k < steps; ++k) {
-          // 64 columns: 32 bytes further inside the swizzled 128-byte row
-          const int t = FMT == BD_FP4_NV ? k : k >> 1;
-          umma_fp4<FMT>(tmem_d, ad + (uint64_t)(2 * k), bdsc + (uint64_t)(2 * k),
-                        FMT == BD_FP4_MX && (k & 1) ? id1 : id0, sfa + 4 * t, sfb + 4 * (t * sfb_tiles),
-                        (i > 0 || k > 0) ? 1u : 0u);
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
         }
-        umma_commit(&empty[s]);
       }
-      umma_commit(done);
-    }
-    __syncwarp();
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
+  } else {
+    pdl_wait();
+    const int64_t t0 = (int64_t)n_blk * p.h;
+    for (int j = threadIdx.x - 64; j < p.h; j += 64) xr[j] = p.x_row && t0 + j < p.tokens ? p.x_row[t0 + j] : 1.f;
   }
 
   const bool ok = mbar_wait(done, 0, nullptr);
@@ -241,7 +353,7 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm(const __grid_constant__ C
   const bool aborted = *abort_flag != 0;
   if (aborted && threadIdx.x == 0) {
     atomicOr(p.status, BD_DEV_TIMEOUT);
-    // every load this CTA issued lands before its shared memory is used again or goes away
+    // every load this CTA issued lands before its shared memory goes away
     const int issued = *issued_out;
     for (int i = max(0, issued - stages); i < issued; ++i)
       mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u, nullptr);
@@ -250,75 +362,362 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm(const __grid_constant__ C
   const int64_t t0 = (int64_t)n_blk * p.h;
   const int n_tok = (int)min((int64_t)p.h, p.tokens - t0);
   const uint32_t lane_addr = tmem_d + ((uint32_t)(warp * 32) << 16);
+  constexpr int kTok = Group<L>::kTok;
+  const int64_t row = m_blk * 128 + threadIdx.x;
+  const bool in = row < p.d_out && !aborted;
+  const float rs = in && p.w_row ? p.w_row[row] : 1.f;
   if (split == 1) {
-    const int64_t row = m_blk * 128 + threadIdx.x;
-    const bool in = row < p.d_out && !aborted;
-    const float rs = in && p.w_row ? p.w_row[row] : 1.f;
-    for (int c0 = 0; c0 < n_tok; c0 += 8) {
-      float v[8];
-      for (int l = 0; l < p.limbs; ++l) {
-        float u[8];
-        tmem_ld8(lane_addr + (uint32_t)(l * p.h + c0), u);
+    for (int c0 = 0; c0 < n_tok; c0 += kTok) {
+      float v[kTok];
+      load_group<L>(lane_addr + (uint32_t)(c0 * L), v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = l == 0 ? u[j] : v[j] + u[j];
+      for (int j = 0; j < kTok; ++j)
+        if (in && c0 + j < n_tok) store_y(p, t0 + c0 + j, row, v[j] * rs * xr[c0 + j]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem_d, tcols);
+    return;
+  }
+  // Token j of the tile belongs to the CTA of rank j % split: each CTA writes its sums into
+  // its owners' shared memory, and after a cluster barrier each adds what it was given in
+  // rank order. The first barrier only says that every CTA has started: they arrive at it
+  // before they ask for tensor memory, so that no CTA waits for another while holding some
+  // (a CTA of this cluster could be waiting for what one of another cluster's holds, and
+  // that one for this).
+  cluster_wait();
+  for (int c0 = 0; c0 < n_tok; c0 += kTok) {
+    float v[kTok];
+    load_group<L>(lane_addr + (uint32_t)(c0 * L), v);
+#pragma unroll
+    for (int j = 0; j < kTok; ++j)
+      if (c0 + j < n_tok) {
+        const int t = c0 + j;
+        st_cluster_f32(map_cluster(smem_u32(gather + ((size_t)rank * share + t / split) * 128 + threadIdx.x),
+                                   (uint32_t)(t % split)),
+                       v[j]);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (in && c0 + j < n_tok) {
-          const int64_t t = t0 + c0 + j;
-          const float o = v[j] * rs * (p.x_row ? p.x_row[t] : 1.f);
-          if (p.y_bf16)
-            reinterpret_cast<uint16_t*>(p.y)[t * p.d_out + row] = (uint16_t)f2bf_bits(o);
-          else
-            reinterpret_cast<float*>(p.y)[t * p.d_out + row] = o;
+  }
+  tc_fence_before();  // tensor memory goes back before the barrier, for the same reason
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem_d, tcols);
+  cluster_arrive();
+  cluster_wait();
+  for (int j = 0; rank + j * split < n_tok; ++j) {
+    float v = 0.f;
+    for (int r = 0; r < split; ++r) v += gather[((size_t)r * share + j) * 128 + threadIdx.x];
+    const int t = rank + j * split;
+    if (in) store_y(p, t0 + t, row, v * rs * xr[t]);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// many X rows: persistent CTA pairs, a tile of 256 W rows x n_tile X rows at a time
+// ------------------------------------------------------------------------------------
+// Each CTA of a pair loads its 128 W rows and half of the X rows (and the scales of its W
+// rows and of all X rows); the even CTA issues the cta_group::2 MMAs for both, and each holds
+// the accumulator of its own W rows. Two accumulators overlap by what the scales take of
+// tensor memory: [0, n_tile) and [n_tile - overlap, ...), so the next tile's MMAs start as
+// soon as the epilogue has read the overlap (the columns that it reads first), and run beside
+// the rest of it.
+constexpr int kPairThreads = 256;       // warp 0 loads, warp 1 MMAs, warps 4-7 epilogue
+constexpr uint32_t kPairSfCol = 448;    // scales in columns 448..511
+constexpr uint32_t kPairOutBytes = 64 * 128 * 4;  // outputs of 64 tokens x 128 rows on their way out
+constexpr int kPairGroupM = 8;          // tiles are walked in bands of this many row blocks
+
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void umma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if (FMT == BD_FP4_NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// arrives on the barrier at this offset in both CTAs when the MMAs issued so far are done
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+template <int FMT, int L>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_fp4_mm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                  const __grid_constant__ CUtensorMap tm_ws, const __grid_constant__ CUtensorMap tm_xs,
+                  const __grid_constant__ CUtensorMap tm_y, const MmArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kTilesPerStage = FMT == BD_FP4_NV ? 4 : 2;
+  constexpr uint32_t kSfBytes = kTilesPerStage * kFp4TileBytes;
+  constexpr uint32_t kNTile = 256 / (8 * L) * (8 * L);       // 256, or 240 with 6 limbs
+  constexpr uint32_t kOverlap = 2 * kNTile - kPairSfCol;     // columns the accumulators share
+  constexpr uint32_t kBBytes = kNTile / 2 * 128;
+  constexpr uint32_t kStage = kMmABytes + kBBytes + 3 * kSfBytes;
+  constexpr uint32_t kSfaCols = kTilesPerStage * 4;
+  constexpr int kGroups = kNTile / Group<L>::kCols;
+  constexpr int kFirst = (kOverlap + Group<L>::kCols - 1) / Group<L>::kCols;  // groups that hold the overlap
+  constexpr int kTok = Group<L>::kTok;
+  constexpr int kOutBufs = 64 / kTok;                        // 2 groups of 32 tokens, or 8 of 8
+  const int stages = p.stages;
+  uint8_t* sa = smem;                                        // [stages] W codes, X codes, scales
+  uint8_t* sb = sa + (size_t)stages * kMmABytes;
+  uint8_t* ss = sb + (size_t)stages * kBBytes;
+  uint8_t* sy = ss + (size_t)stages * 3 * kSfBytes;          // [kOutBufs] groups of finished outputs
+  uint64_t* full = reinterpret_cast<uint64_t*>(sy + kPairOutBytes);
+  uint64_t* empty = full + stages;
+  uint64_t* acc_full = empty + stages;  // [2] an accumulator is complete (both CTAs)
+  uint64_t* drained = acc_full + 2;     // the overlap of the current tile has been read (even CTA)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int cta = (int)cluster_rank();
+  const bool leader = cta == 0;
+  const int tiles_m = (int)((p.d_out + 255) / 256);
+  const int64_t tiles = (int64_t)tiles_m * p.tiles_n;
+  const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
+  // tile i of the walk: bands of kPairGroupM row blocks, all N tiles of a band before the next
+  auto tile_of = [&](int64_t i, int& m, int& n) {
+    const int64_t band = i / ((int64_t)kPairGroupM * p.tiles_n);
+    const int rows = min(kPairGroupM, tiles_m - (int)band * kPairGroupM);
+    const int64_t r = i - band * kPairGroupM * p.tiles_n;
+    m = (int)band * kPairGroupM + (int)(r % rows);
+    n = (int)(r / rows);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full[0], 1);
+    mbar_init(&acc_full[1], 1);
+    mbar_init(drained, 8);  // four epilogue warps of each CTA
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_ws);
+    tma_prefetch_desc(&tm_xs);
+    if (p.y_tma) tma_prefetch_desc(&tm_y);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // the pair's barriers and tensor memory are ready
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  bool timed_out = false;
+  if (warp == 0) {
+    int it = 0, s = 0;  // stages used so far, stage of the ring
+    uint32_t ph = 1;    // a fresh barrier's "previous" phase counts as complete
+    const uint32_t full0 = map_cluster(smem_u32(full), 0);
+    for (int64_t i = pair; i < tiles && !timed_out; i += pairs) {
+      int m, n;
+      tile_of(i, m, n);
+      const int w_row0 = m * 256 + cta * 128;
+      const int x_row0 = n * p.n_stride;
+      const int w_tile0 = (w_row0 >> 7) * p.tiles_kw, x_tile0 = (x_row0 >> 7) * p.tiles_kw;
+      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+        if (!mbar_wait(&empty[s], ph, abort_flag)) {
+          timed_out = true;
+          break;
+        }
+        if (elect_one()) {
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          const uint32_t bar = full0 + 8 * s;
+          uint8_t* sf = ss + (size_t)s * 3 * kSfBytes;
+          const int t0 = kb * kTilesPerStage;
+          tma_load_2d_pair(sa + (size_t)s * kMmABytes, &tm_w, bar, kb * 128, w_row0);
+          tma_load_2d_pair(sb + (size_t)s * kBBytes, &tm_x, bar, kb * 128, x_row0 + cta * (int)(kNTile / 2));
+          tma_load_2d_pair(sf, &tm_ws, bar, 0, w_tile0 + t0);
+          tma_load_2d_pair(sf + kSfBytes, &tm_xs, bar, 0, x_tile0 + t0);
+          tma_load_2d_pair(sf + 2 * kSfBytes, &tm_xs, bar, 0, x_tile0 + p.tiles_kw + t0);
+        }
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
         }
       }
     }
-  } else {
-    // sums [token][128 rows] in the (now unused) stage buffers
-    __syncthreads();
-    float* part = reinterpret_cast<float*>(smem);
-    for (int c0 = 0; c0 < n_tok; c0 += 8) {
-      float v[8];
-      for (int l = 0; l < p.limbs; ++l) {
-        float u[8];
-        tmem_ld8(lane_addr + (uint32_t)(l * p.h + c0), u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = l == 0 ? u[j] : v[j] + u[j];
+    // all MMAs that read this CTA's shared memory are over before it leaves (bounded)
+    for (int k = max(0, it - stages); k < it; ++k)
+      if (!mbar_wait(&empty[k % stages], (uint32_t)(k / stages) & 1u, abort_flag)) timed_out = true;
+    if (timed_out) *abort_flag = 1;
+  } else if (warp == 1 && leader) {
+    const uint32_t id0 = umma_idesc_fp4(256, kNTile, FMT == BD_FP4_MX, 0);
+    const uint32_t id1 = umma_idesc_fp4(256, kNTile, FMT == BD_FP4_MX, 2);
+    const uint32_t sfa = tmem + kPairSfCol, sfb = sfa + kSfaCols;
+    const uint64_t ad0 = umma_desc_sw128(smem_u32(sa)), bd0 = umma_desc_sw128(smem_u32(sb));
+    const uint64_t sd0 = scale_desc(smem_u32(ss));
+    int s = 0, j = 0;  // stage of the ring, tiles so far
+    uint32_t ph = 0;
+    for (int64_t i = pair; i < tiles && !timed_out; i += pairs, ++j) {
+      if (j > 0) {
+        if (!mbar_wait(drained, (uint32_t)(j - 1) & 1u, abort_flag)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after();
       }
+      const uint32_t d = tmem + (j & 1 ? kNTile - kOverlap : 0);
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!mbar_wait(&full[s], ph, abort_flag)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t ad = ad0 + (uint32_t)s * (kMmABytes >> 4), bdsc = bd0 + (uint32_t)s * (kBBytes >> 4);
+          const uint64_t sd = sd0 + (uint32_t)s * (3 * kSfBytes >> 4);
+          const int steps = p.k_steps - kb * 4;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c0 + j < n_tok) part[(c0 + j) * 128 + threadIdx.x] = v[j];
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) {
+              const int t = FMT == BD_FP4_NV ? k : k >> 1;
+              if (FMT == BD_FP4_NV || (k & 1) == 0) {
+                tmem_cp_scales_pair(sfa + 4 * t, sd + t * (kFp4TileBytes >> 4));
+                tmem_cp_scales_pair(sfb + 8 * t, sd + ((kSfBytes + t * kFp4TileBytes) >> 4));
+                tmem_cp_scales_pair(sfb + 8 * t + 4, sd + ((2 * kSfBytes + t * kFp4TileBytes) >> 4));
+              }
+              umma_fp4_pair<FMT>(d, ad + 2 * k, bdsc + 2 * k, FMT == BD_FP4_MX && (k & 1) ? id1 : id0, sfa + 4 * t,
+                                 sfb + 8 * t, k > 0 ? 1u : (kb > 0 ? 1u : 0u));
+            }
+          umma_commit_pair(&empty[s]);
+        }
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+      if (elect_one()) umma_commit_pair(&acc_full[j & 1]);
+      __syncwarp();
     }
-    // tensor memory goes back before the CTAs wait for one another: a CTA that held it while
-    // waiting could keep one of another cluster's CTAs, and so that cluster, from starting
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem_d, tcols);
-    cluster_sync_all();
-    const int64_t row = m_blk * 128 + threadIdx.x;
-    const bool in = row < p.d_out && !aborted;
-    const float rs = in && p.w_row ? p.w_row[row] : 1.f;
-    for (int j = rank; j < n_tok; j += split) {
-      const uint32_t at = smem_u32(part + j * 128 + threadIdx.x);
-      float v = 0.f;
-      for (int r = 0; r < split; ++r) v += ld_cluster_f32(at, (uint32_t)r);
-      if (in) {
-        const int64_t t = t0 + j;
-        const float o = v * rs * (p.x_row ? p.x_row[t] : 1.f);
-        if (p.y_bf16)
-          reinterpret_cast<uint16_t*>(p.y)[t * p.d_out + row] = (uint16_t)f2bf_bits(o);
-        else
-          reinterpret_cast<float*>(p.y)[t * p.d_out + row] = o;
+    if (timed_out) *abort_flag = 1;
+  } else if (warp >= 4) {
+    const int w = warp - 4;
+    const uint32_t drained_bar = map_cluster(smem_u32(drained), 0);
+    const int r0 = w * 32 + lane;  // row of this CTA's half of the tile
+    int j = 0, out = 0;            // tiles and groups so far
+    for (int64_t i = pair; i < tiles; i += pairs, ++j) {
+      int m, n;
+      tile_of(i, m, n);
+      const int64_t row0 = (int64_t)m * 256 + cta * 128, row = row0 + r0;
+      const bool in = row < p.d_out;
+      const float rs = in && p.w_row ? p.w_row[row] : 1.f;
+      const int64_t t0 = (int64_t)n * p.h;
+      float xs = 1.f;  // lane k holds the scale of token g * kTok + k of the next group
+      auto token_scale = [&](int g) {
+        const int64_t t = t0 + (int64_t)g * kTok + lane;
+        return p.x_row && lane < kTok && t < p.tokens ? p.x_row[t] : 1.f;
+      };
+      // the overlap lies at the end of the even accumulator and at the start of the odd one
+      auto group_of = [&](int q) { return (j & 1) ? q : kGroups - 1 - q; };
+      xs = token_scale(group_of(0));
+      if (!mbar_wait(&acc_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag)) {
+        timed_out = true;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t at = tmem + (j & 1 ? kNTile - kOverlap : 0) + ((uint32_t)(w * 32) << 16);
+      for (int q = 0; q < kGroups; ++q) {
+        const int g = group_of(q);
+        const int64_t tg = t0 + (int64_t)g * kTok;
+        float v[kTok];
+        load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
+        if (q == kFirst - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(drained_bar);
+        }
+        const float xg = xs;
+        if (q + 1 < kGroups) xs = token_scale(group_of(q + 1));
+#pragma unroll
+        for (int c = 0; c < kTok; ++c) v[c] = v[c] * rs * __shfl_sync(0xffffffffu, xg, c);
+        if (p.y_tma) {
+          // [token][128 rows] in shared memory, then one bulk store of the group; a buffer is
+          // written again only after the store that read it (waited for before the barrier
+          // that every writer passes)
+          uint8_t* buf = sy + (size_t)(out % kOutBufs) * (kTok * 128 * 4);
+          if (p.y_bf16) {
+#pragma unroll
+            for (int c = 0; c < kTok; ++c)
+              reinterpret_cast<uint16_t*>(buf)[c * 128 + r0] = (uint16_t)f2bf_bits(v[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < kTok; ++c) reinterpret_cast<float*>(buf)[c * 128 + r0] = v[c];
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 2) : "memory");
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (w == 0 && lane == 0) {
+            if (row0 < p.d_out && tg < p.tokens) tma_store_2d(&tm_y, buf, (int)row0, (int)tg);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          ++out;
+        } else {
+          const int n_tok = (int)min((int64_t)kTok, p.tokens - tg);
+#pragma unroll
+          for (int c = 0; c < kTok; ++c)
+            if (in && c < n_tok) store_y(p, tg + c, row, v[c]);
+        }
       }
     }
-    cluster_sync_all();  // no CTA leaves while another reads its shared memory
+    if (p.y_tma && w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (timed_out) *abort_flag = 1;
   }
-  if (split == 1) {
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem_d, tcols);
-  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, BD_DEV_TIMEOUT);
+  cluster_arrive();  // neither CTA leaves while the other's MMAs or barriers may reach it
+  cluster_wait();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // ------------------------------------------------------------------------------------
@@ -336,49 +735,123 @@ static bool encode_codes(CUtensorMap* m, const void* base, int64_t rows, int64_t
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the tiled scales as rows of one tile (128 words), so that a stage's tiles are one box
+static bool encode_scales(CUtensorMap* m, const void* base, int64_t tiles, int box_tiles) {
+  TensorMapEncodeFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {128, (cuuint64_t)tiles};
+  cuuint64_t strides[1] = {(cuuint64_t)kFp4TileBytes};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_tiles};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y [tokens][d_out], boxes of 128 columns x box_tokens rows
+static bool encode_out(CUtensorMap* m, const MmArgs& a, int box_tokens) {
+  TensorMapEncodeFn enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)a.d_out, (cuuint64_t)a.tokens};
+  cuuint64_t strides[1] = {(cuuint64_t)a.d_out * (a.y_bf16 ? 2 : 4)};
+  cuuint32_t box[2] = {128u, (cuuint32_t)box_tokens};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.y, dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt) {
-  Fp4Plan p;
+  Fp4Plan p = {};
   p.limbs = limbs;
-  // tokens of an N tile: as many as fit 256 X rows, in steps of 8 (16 without limbs), all
-  // tokens in one tile when they fit
-  const int step = limbs > 1 ? 8 : 16;
-  const int most = limbs > 1 ? 256 / limbs / 8 * 8 : 256;
-  p.h = (int)((tokens + step - 1) / step * step);
-  if (p.h > most) p.h = most;
-  if (limbs == 1 && p.h > 128) p.h = 256;  // X rows of a tile start at a scale tile
-  p.n_tile = p.h * limbs;
-  p.n_stride = limbs > 1 ? (p.n_tile + 127) / 128 * 128 : p.n_tile;
-  p.tiles_n = (int)((tokens + p.h - 1) / p.h);
-  p.tiles_m = (int)((d_out + 127) / 128);
   p.kblocks = (int)((d_in + kFp4KStage - 1) / kFp4KStage);
+  const int sf = (fmt == BD_FP4_NV ? 4 : 2) * kFp4TileBytes;
+  // tokens of an N tile of at most 256 X rows: in steps of 8 with limbs, 16 without
+  const int step = limbs > 1 ? 8 : 16;
+  const int most = 256 / (8 * limbs) * 8;
+  p.pair = tokens > most;
+  if (p.pair) {
+    p.h = most;
+    p.n_tile = p.h * limbs;
+    p.n_stride = 256;
+    p.tiles_n = (int)((tokens + p.h - 1) / p.h);
+    p.tiles_m = (int)((d_out + 255) / 256);
+    const size_t stage = kMmABytes + (size_t)p.n_tile * 64 + 3 * (size_t)sf;
+    p.stages = (int)((226 * 1024 - 1024 - kPairOutBytes) / stage);
+    p.split = 1;
+    p.smem = 1024 + p.stages * stage + kPairOutBytes + (2 * p.stages + 3) * 8 + 16;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2;
+    p.ctas = 2 * (tiles < pairs ? tiles : pairs);
+  } else {
+    p.h = (int)((tokens + step - 1) / step * step);
+    if (p.h > 128) p.h = 128;  // a cluster keeps h * 128 sums in each CTA's shared memory
+    p.n_tile = p.h * limbs;
+    p.n_stride = (p.n_tile + 127) / 128 * 128;
+    p.tiles_n = (int)((tokens + p.h - 1) / p.h);
+    p.tiles_m = (int)((d_out + 127) / 128);
+    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m;
+    p.split = 1;
+    while (p.split < 8 && p.split * 2 <= p.kblocks && tiles * p.split < sm_count()) p.split *= 2;
+    const size_t stage = kMmABytes + (size_t)p.n_tile * 128 + (size_t)sf * (1 + (p.n_tile + 127) / 128);
+    const size_t gather = p.split > 1 ? (size_t)p.split * ((p.h + p.split - 1) / p.split) * 512 : 0;
+    const size_t fixed = 1024 + gather + (size_t)p.h * 4 + 17 * 8 + 16;
+    int st = (int)((220 * 1024 - fixed) / stage);
+    const int need = (p.kblocks + p.split - 1) / p.split;
+    if (st > need) st = need;
+    if (st > 8) st = 8;
+    p.stages = st;
+    p.smem = fixed + st * stage;
+    p.ctas = tiles * p.split;
+  }
   p.x_rows = limbs > 1 ? (int64_t)p.tiles_n * p.n_stride : tokens;
   p.xc_bytes = limbs > 1 ? align_up((size_t)p.x_rows * (size_t)(d_in / 2), 256) : 0;
   p.xs_bytes = limbs > 1 ? (size_t)fp4_scale_bytes(p.x_rows, d_in, fmt) : 0;
-  const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m;
-  p.split = 1;
-  while (p.split < 8 && p.split * 2 <= p.kblocks && tiles * p.split < sm_count()) p.split *= 2;
-  const int sf = (fmt == BD_FP4_NV ? 4 : 2) * kFp4TileBytes;
-  const size_t stage = kMmABytes + (size_t)p.n_tile * 128 + (size_t)sf * (1 + (p.n_tile + 127) / 128);
-  int st = (int)((200 * 1024) / stage);
-  const int need = (p.kblocks + p.split - 1) / p.split;
-  if (st > need) st = need;
-  if (st > 8) st = 8;
-  p.stages = st;
-  size_t bytes = (size_t)st * stage;
-  if (p.split > 1 && bytes < (size_t)p.h * 512) bytes = (size_t)p.h * 512;
-  p.smem = 1024 + bytes + (2 * st + 1) * 8 + 16;
   return p;
 }
 
+namespace {
+template <int FMT, int L>
+bd_status launch_mm(const Fp4Plan& p, const Fp4Mat& w, const Fp4Mat& x, const MmArgs& a, int64_t d_in,
+                    cudaStream_t s) {
+  CUtensorMap tw, tx;
+  if (!encode_codes(&tw, w.codes, a.d_out, d_in / 2, 128)) return BD_ERR_CUDA;
+  if (!encode_codes(&tx, x.codes, p.x_rows, d_in / 2, p.pair ? p.n_tile / 2 : p.n_tile)) return BD_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(p.pair ? kPairThreads : kMmThreads);
+  cfg.dynamicSmemBytes = p.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)(p.pair ? 2 : p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  static std::atomic<uint64_t> attr_rows{0}, attr_pair{0};
+  if (p.pair) {
+    CUtensorMap tws, txs;
+    const int box = FMT == BD_FP4_NV ? 4 : 2;
+    if (!encode_scales(&tws, w.scales, (a.d_out + 127) / 128 * a.tiles_kw, box) ||
+        !encode_scales(&txs, x.scales, (int64_t)a.x_row_tiles * a.tiles_kw, box))
+      return BD_ERR_CUDA;
+    CUtensorMap ty = {};
+    if (a.y_tma && !encode_out(&ty, a, Group<L>::kTok)) return BD_ERR_CUDA;
+    if (!ensure_dyn_smem(k_fp4_mm_pair<FMT, L>, 227 * 1024, attr_pair)) return BD_ERR_CUDA;
+    BD_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_fp4_mm_pair<FMT, L>, tw, tx, tws, txs, ty, a));
+  } else {
+    if (!ensure_dyn_smem(k_fp4_mm_rows<FMT, L>, 227 * 1024, attr_rows)) return BD_ERR_CUDA;
+    BD_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_fp4_mm_rows<FMT, L>, tw, tx, a));
+  }
+  return BD_OK;
+}
+}  // namespace
+
 bd_status launch_fp4_mm(const Fp4Plan& p, int fmt, const Fp4Mat& w, const Fp4Mat& x, int64_t d_out, int64_t d_in,
                         int64_t tokens, void* y, int32_t y_dtype, uint32_t* status, cudaStream_t s) {
-  CUtensorMap tw, tx;
-  if (!encode_codes(&tw, w.codes, d_out, d_in / 2, 128)) return BD_ERR_CUDA;
-  if (!encode_codes(&tx, x.codes, p.x_rows, d_in / 2, p.n_tile)) return BD_ERR_CUDA;
-  static std::atomic<uint64_t> attr_nv{0}, attr_mx{0};
-  auto* fn = fmt == BD_FP4_NV ? k_fp4_mm<BD_FP4_NV> : k_fp4_mm<BD_FP4_MX>;
-  if (!ensure_dyn_smem(fn, 227 * 1024, fmt == BD_FP4_NV ? attr_nv : attr_mx)) return BD_ERR_CUDA;
-  MmArgs a;
+  MmArgs a = {};
   a.w_scales = w.scales;
   a.x_scales = x.scales;
   a.w_row = w.row;
@@ -388,32 +861,31 @@ bd_status launch_fp4_mm(const Fp4Plan& p, int fmt, const Fp4Mat& w, const Fp4Mat
   a.d_out = d_out;
   a.tokens = tokens;
   a.tiles_kw = (int)fp4_tiles_k(d_in, fmt);
-  a.limbs = p.limbs;
+  a.x_row_tiles = (int)((p.x_rows + 127) / 128);
   a.h = p.h;
   a.n_tile = p.n_tile;
   a.n_stride = p.n_stride;
+  a.tiles_n = p.tiles_n;
   a.kblocks = p.kblocks;
   a.k_steps = (int)((d_in + 63) / 64);
   a.split = p.split;
   a.stages = p.stages;
   a.y_bf16 = y_dtype == BD_BF16;
-  a.x_row_tiles = (int)((p.x_rows + 127) / 128);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.tiles_m * p.tiles_n * p.split));
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)p.split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  // the limbs kernel goes before: its blocks start the next kernel after they have waited for
+  // everything earlier on the stream, and it does not write W
+  a.w_early = p.limbs > 1;
+  a.y_tma = (d_out * (a.y_bf16 ? 2 : 4)) % 16 == 0;
   launch_begin(K_FP4_MM, s);
-  BD_CUDA_TRY(cudaLaunchKernelEx(&cfg, fn, tw, tx, a));
+  bd_status r;
+  if (fmt == BD_FP4_NV)
+    r = p.limbs == 1   ? launch_mm<BD_FP4_NV, 1>(p, w, x, a, d_in, s)
+        : p.limbs == 4 ? launch_mm<BD_FP4_NV, kFp4LimbsBf16>(p, w, x, a, d_in, s)
+                       : launch_mm<BD_FP4_NV, kFp4LimbsF32>(p, w, x, a, d_in, s);
+  else
+    r = p.limbs == 1   ? launch_mm<BD_FP4_MX, 1>(p, w, x, a, d_in, s)
+        : p.limbs == 4 ? launch_mm<BD_FP4_MX, kFp4LimbsBf16>(p, w, x, a, d_in, s)
+                       : launch_mm<BD_FP4_MX, kFp4LimbsF32>(p, w, x, a, d_in, s);
+  if (r != BD_OK) return r;
   launch_end(K_FP4_MM, s);
   BD_LAUNCH_CHECK();
   return BD_OK;
