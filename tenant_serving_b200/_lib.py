@@ -427,26 +427,63 @@ def bd_apply_multi_fp8(w_codes, w_scales, table, tenant_ids, x, y=None, y_dtype=
     return y, workspace
 
 
-class _here:
-    """Makes the device that holds all of a call's tensors the current one for the call (and
-    so its current stream the default); refuses tensors that live apart."""
+# The 4-bit calls below are also made for single tokens, where the host's time per call counts:
+# they read tensor properties once and pass plain integers.
+_FP4_BLOCK = {BD_FP4_NV: 16, BD_FP4_MX: 32}
 
-    def __init__(self, *ts):
-        torch = _torch()
-        ts = [t for t in ts if t is not None]
-        _require_cuda(*ts)
-        dev = ts[0].device
-        if any(t.device != dev for t in ts):
-            raise ValueError("the tensors of a call live on one GPU")
-        self._ctx = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+class _Current:
+    """Makes another device than the current one current for a call."""
+
+    def __init__(self, index):
+        self._ctx = _torch().cuda.device(index)
 
     def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
+        self._ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+        self._ctx.__exit__(*exc)
+
+
+def _on_device(ts):
+    """Index of the GPU that holds all of a call's tensors (None entries aside)."""
+    dev = -1
+    for t in ts:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("tensors passed to the library must live on the GPU")
+            if d != dev and dev >= 0:
+                raise ValueError("the tensors of a call live on one GPU")
+            dev = d
+    return dev
+
+
+def _raw_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    try:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    except AttributeError:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _fp4_call(name, dev, args, stream):
+    """Calls an entry point with its device current and that device's stream as last argument."""
+    torch = _torch()
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, _raw_stream(stream, dev))
+    else:
+        with _Current(dev):
+            rc = fn(*args, _raw_stream(stream, dev))
+    if rc != BD_OK:
+        raise BitDeltaError(rc, name)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
 
 
 def bd_fp4_scales_bytes(rows, cols, fmt) -> int:
@@ -479,23 +516,27 @@ def fp4_workspace(nbytes, device):
 def _fp4_shape(codes, scales, row_scales, fmt, where):
     """[rows, cols] of a packed matrix, its buffers' sizes and types checked."""
     torch = _torch()
+    if fmt not in _FP4_BLOCK:
+        raise BitDeltaError(BD_ERR_CONFIG, where)
+    u8 = torch.uint8
+    if codes.dtype is not u8 or scales.dtype is not u8 or (row_scales is not None and row_scales.dtype is not torch.float32):
+        raise TypeError(f"{where}: codes and scales are uint8, row scales float32")
+    if not (codes.is_contiguous() and scales.is_contiguous()) or (row_scales is not None and not row_scales.is_contiguous()):
+        raise ValueError(f"{where}: packed matrices are contiguous")
     rows, half = codes.shape
-    for t, dt in ((codes, torch.uint8), (scales, torch.uint8), (row_scales, torch.float32)):
-        if t is not None and t.dtype != dt:
-            raise TypeError(f"{where}: codes and scales are uint8, row scales float32")
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{where}: packed matrices are contiguous")
-    n = bd_fp4_scales_bytes(rows, 2 * half, fmt)
-    if n == 0 or scales.numel() != n or (row_scales is not None and row_scales.numel() != rows):
+    cols = 2 * half
+    per = 4 * _FP4_BLOCK[fmt]
+    if rows < 1 or cols < 32 or cols % 32 or scales.numel() != -(-rows // 128) * -(-cols // per) * 512 or \
+            (row_scales is not None and row_scales.numel() != rows):
         raise BitDeltaError(BD_ERR_SHAPE, where)
-    return rows, 2 * half
+    return rows, cols
 
 
-def _fp4_out(y, shape, dtype, device, where):
-    torch = _torch()
+def _fp4_out(y, rows, cols, dtype, like, where):
     if y is None:
-        return torch.empty(shape, dtype=dtype or torch.bfloat16, device=device)
-    if tuple(y.shape) != tuple(shape) or not y.is_contiguous():
+        torch = _torch()
+        return torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=like.device)
+    if y.dim() != 2 or y.size(0) != rows or y.size(1) != cols or not y.is_contiguous():
         raise BitDeltaError(BD_ERR_SHAPE, where)
     return y
 
@@ -504,18 +545,15 @@ def bd_prepare_fp4_scales(scales, fmt, rows, cols, out=None, stream=None):
     """Wrap ``bd_prepare_fp4_scales``: row-major block scales (uint8, or a float8 dtype of the
     same bytes) -> the tiled layout."""
     torch = _torch()
-    here = _here(scales, out)
-    shape = fp4_scales_shape(rows, cols, fmt) if bd_fp4_scales_bytes(rows, cols, fmt) else None
-    if shape is None or scales.element_size() != 1 or not scales.is_contiguous() or \
-            scales.numel() != rows * (cols // (16 if fmt == BD_FP4_NV else 32)):
-        raise BitDeltaError(BD_ERR_SHAPE, "bd_prepare_fp4_scales")
-    if out is None:
-        out = torch.empty(shape, dtype=torch.uint8, device=scales.device)
-    elif out.numel() != bd_fp4_scales_bytes(rows, cols, fmt) or not out.is_contiguous():
-        raise BitDeltaError(BD_ERR_SHAPE, "bd_prepare_fp4_scales")
-    with here:
-        rc = lib().bd_prepare_fp4_scales(_ptr(scales), int(fmt), int(rows), int(cols), _ptr(out), _stream(stream))
-    check(rc, "bd_prepare_fp4_scales")
+    where = "bd_prepare_fp4_scales"
+    n = bd_fp4_scales_bytes(rows, cols, fmt)
+    if out is None and n and scales.is_cuda:
+        out = torch.empty(fp4_scales_shape(rows, cols, fmt), dtype=torch.uint8, device=scales.device)
+    dev = _on_device((scales, out))
+    if n == 0 or scales.element_size() != 1 or not scales.is_contiguous() or not out.is_contiguous() or \
+            scales.numel() != rows * (cols // _FP4_BLOCK[fmt]) or out.numel() * out.element_size() != n:
+        raise BitDeltaError(BD_ERR_SHAPE, where)
+    _fp4_call(where, dev, (_p(scales), int(fmt), int(rows), int(cols), _p(out)), stream)
     return out
 
 
@@ -523,37 +561,31 @@ def bd_quantize_fp4(x, fmt, codes=None, scales=None, row_scales=None, hat=None, 
     """Wrap ``bd_quantize_fp4``: (codes uint8 [rows, cols/2], tiled scales uint8, row scales
     fp32 [rows] or None for BD_FP4_MX, x_hat or None). ``x`` may have any row stride; x_hat is
     written when ``hat`` or ``hat_dtype`` is given."""
-    torch = _torch()
-    here = _here(x, codes, scales, row_scales, hat)
+    where = "bd_quantize_fp4"
+    dev = _on_device((x, codes, scales, row_scales, hat))
     rows, cols = x.shape
-    if x.stride(1) != 1 and cols > 1:
-        raise BitDeltaError(BD_ERR_SHAPE, "bd_quantize_fp4")
+    if cols > 1 and x.stride(1) != 1:
+        raise BitDeltaError(BD_ERR_SHAPE, where)
     if codes is None or scales is None or (row_scales is None and fmt == BD_FP4_NV):
         c, s, r = fp4_buffers(rows, cols, fmt, x.device)
         codes, scales, row_scales = (codes if codes is not None else c), (scales if scales is not None else s), \
             (row_scales if row_scales is not None else r)
-    if tuple(codes.shape) != (rows, cols // 2):
-        raise BitDeltaError(BD_ERR_SHAPE, "bd_quantize_fp4")
-    _fp4_shape(codes, scales, row_scales, fmt, "bd_quantize_fp4")
+    if _fp4_shape(codes, scales, row_scales, fmt, where) != (rows, cols):
+        raise BitDeltaError(BD_ERR_SHAPE, where)
     if hat is not None or hat_dtype is not None:
-        hat = _fp4_out(hat, (rows, cols), hat_dtype, x.device, "bd_quantize_fp4")
-    with here:
-        rc = lib().bd_quantize_fp4(_ptr(x), dtype_code(x), rows, cols, x.stride(0) if rows > 1 else cols, int(fmt),
-                                   _ptr(codes), _ptr(scales), _ptr(row_scales), _ptr(hat),
-                                   dtype_code(hat) if hat is not None else BD_F32, _stream(stream))
-    check(rc, "bd_quantize_fp4")
+        hat = _fp4_out(hat, rows, cols, hat_dtype, x, where)
+    _fp4_call(where, dev, (_p(x), dtype_code(x), rows, cols, x.stride(0) if rows > 1 else cols, fmt, _p(codes),
+                           _p(scales), _p(row_scales), _p(hat), dtype_code(hat) if hat is not None else BD_F32), stream)
     return codes, scales, row_scales, hat
 
 
 def bd_dequantize_fp4(codes, scales, row_scales, fmt, out=None, out_dtype=None, stream=None):
     """Wrap ``bd_dequantize_fp4``: the values of a packed matrix, bf16 unless asked otherwise."""
-    here = _here(codes, scales, row_scales, out)
-    rows, cols = _fp4_shape(codes, scales, row_scales, fmt, "bd_dequantize_fp4")
-    out = _fp4_out(out, (rows, cols), out_dtype, codes.device, "bd_dequantize_fp4")
-    with here:
-        rc = lib().bd_dequantize_fp4(_ptr(codes), _ptr(scales), _ptr(row_scales), int(fmt), rows, cols, _ptr(out),
-                                     dtype_code(out), _stream(stream))
-    check(rc, "bd_dequantize_fp4")
+    where = "bd_dequantize_fp4"
+    dev = _on_device((codes, scales, row_scales, out))
+    rows, cols = _fp4_shape(codes, scales, row_scales, fmt, where)
+    out = _fp4_out(out, rows, cols, out_dtype, codes, where)
+    _fp4_call(where, dev, (_p(codes), _p(scales), _p(row_scales), fmt, rows, cols, _p(out), dtype_code(out)), stream)
     return out
 
 
@@ -565,19 +597,17 @@ def bd_matmul_fp4(w_codes, w_scales, w_row, x_codes, x_scales, x_row, fmt, y=Non
                   stream=None):
     """Wrap ``bd_matmul_fp4``: (y [tokens, d_out], workspace) with y = X_hat W_hat^T. A workspace
     of the caller's is zeroed once before its first use (``fp4_workspace``)."""
-    here = _here(w_codes, w_scales, w_row, x_codes, x_scales, x_row, y, workspace)
-    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, "bd_matmul_fp4")
-    tokens = x_codes.shape[0]
-    if tokens and _fp4_shape(x_codes, x_scales, x_row, fmt, "bd_matmul_fp4") != (tokens, d_in):
-        raise BitDeltaError(BD_ERR_SHAPE, "bd_matmul_fp4")
-    y = _fp4_out(y, (tokens, d_out), y_dtype, w_codes.device, "bd_matmul_fp4")
+    where = "bd_matmul_fp4"
+    dev = _on_device((w_codes, w_scales, w_row, x_codes, x_scales, x_row, y, workspace))
+    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, where)
+    tokens = x_codes.size(0)
+    if tokens and _fp4_shape(x_codes, x_scales, x_row, fmt, where) != (tokens, d_in):
+        raise BitDeltaError(BD_ERR_SHAPE, where)
+    y = _fp4_out(y, tokens, d_out, y_dtype, w_codes, where)
     if workspace is None:
         workspace = fp4_workspace(bd_matmul_fp4_workspace_size(d_out, d_in, tokens), w_codes.device)
-    with here:
-        rc = lib().bd_matmul_fp4(_ptr(w_codes), _ptr(w_scales), _ptr(w_row), _ptr(x_codes), _ptr(x_scales), _ptr(x_row),
-                                 int(fmt), d_out, d_in, tokens, _ptr(y), dtype_code(y), _ptr(workspace),
-                                 workspace.numel(), _stream(stream))
-    check(rc, "bd_matmul_fp4")
+    _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), _p(x_codes), _p(x_scales), _p(x_row), fmt, d_out,
+                           d_in, tokens, _p(y), dtype_code(y), _p(workspace), workspace.nbytes), stream)
     return y, workspace
 
 
@@ -586,27 +616,25 @@ def bd_linear_fp4_workspace_size(d_out, d_in, tokens) -> int:
 
 
 def _bf16_rows(x, d_in, where):
-    torch = _torch()
-    if x.dtype != torch.bfloat16:
+    if x.dtype is not _torch().bfloat16:
         raise TypeError(f"{where}: activations are bfloat16")
-    if x.dim() != 2 or x.shape[1] != d_in or not x.is_contiguous():
+    if x.dim() != 2 or x.size(1) != d_in or not x.is_contiguous():
         raise BitDeltaError(BD_ERR_SHAPE, where)
-    return x.shape[0]
+    return x.size(0)
 
 
 def bd_linear_fp4(w_codes, w_scales, w_row, x, fmt, y=None, y_dtype=None, workspace=None, stream=None):
     """Wrap ``bd_linear_fp4``: (y [tokens, d_out], workspace) with y = x W_hat^T, x bf16."""
-    torch = _torch()
-    here = _here(w_codes, w_scales, w_row, x, y, workspace)
-    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, "bd_linear_fp4")
-    tokens = _bf16_rows(x, d_in, "bd_linear_fp4")
-    y = _fp4_out(y, (tokens, d_out), y_dtype, x.device, "bd_linear_fp4")
+    where = "bd_linear_fp4"
+    dev = _on_device((w_codes, w_scales, w_row, x, y, workspace))
+    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, where)
+    tokens = _bf16_rows(x, d_in, where)
+    y = _fp4_out(y, tokens, d_out, y_dtype, x, where)
     if workspace is None:
+        torch = _torch()
         workspace = torch.empty(bd_linear_fp4_workspace_size(d_out, d_in, tokens), dtype=torch.uint8, device=x.device)
-    with here:
-        rc = lib().bd_linear_fp4(_ptr(w_codes), _ptr(w_scales), _ptr(w_row), int(fmt), d_out, d_in, _ptr(x), tokens,
-                                 _ptr(y), dtype_code(y), _ptr(workspace), workspace.numel(), _stream(stream))
-    check(rc, "bd_linear_fp4")
+    _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), fmt, d_out, d_in, _p(x), tokens, _p(y),
+                           dtype_code(y), _p(workspace), workspace.nbytes), stream)
     return y, workspace
 
 
@@ -618,21 +646,21 @@ def bd_apply_multi_fp4(w_codes, w_scales, w_row, table, tenant_ids, x, fmt, y=No
                        stream=None):
     """Wrap ``bd_apply_multi_fp4``: y[t] = W_hat x[t] + Delta_hat_{ids[t]} x[t], W_hat a
     microscaled 4-bit base."""
+    where = "bd_apply_multi_fp4"
     torch = _torch()
-    here = _here(w_codes, w_scales, w_row, table.dev, tenant_ids, x, y, workspace)
-    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, "bd_apply_multi_fp4")
-    batch = _bf16_rows(x, d_in, "bd_apply_multi_fp4")
-    if tenant_ids.dtype != torch.int32 or tenant_ids.numel() != batch:
-        raise BitDeltaError(BD_ERR_SHAPE, "bd_apply_multi_fp4")
-    y = _fp4_out(y, (batch, d_out), y_dtype, x.device, "bd_apply_multi_fp4")
+    tab = table.ptr().value or 0
+    dev = _on_device((w_codes, w_scales, w_row, tenant_ids, x, y, workspace, getattr(table, "dev", None)))
+    d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, where)
+    batch = _bf16_rows(x, d_in, where)
+    if tenant_ids.dtype is not torch.int32 or tenant_ids.numel() != batch or not tenant_ids.is_contiguous():
+        raise BitDeltaError(BD_ERR_SHAPE, where)
+    y = _fp4_out(y, batch, d_out, y_dtype, x, where)
     if workspace is None:
         workspace = torch.empty(max(bd_apply_fp4_workspace_size(d_out, d_in, batch, table.n), 16),
                                 dtype=torch.uint8, device=x.device)
-    with here:
-        rc = lib().bd_apply_multi_fp4(_ptr(w_codes), _ptr(w_scales), _ptr(w_row), int(fmt), d_out, d_in, table.ptr(),
-                                      table.n, table.scale_dtype, _ptr(tenant_ids), _ptr(x), batch, _ptr(y),
-                                      dtype_code(y), _ptr(workspace), workspace.numel(), _stream(stream))
-    check(rc, "bd_apply_multi_fp4")
+    _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), fmt, d_out, d_in, tab, table.n, table.scale_dtype,
+                           _p(tenant_ids), _p(x), batch, _p(y), dtype_code(y), _p(workspace), workspace.nbytes),
+              stream)
     return y, workspace
 
 

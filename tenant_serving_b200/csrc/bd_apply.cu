@@ -333,7 +333,7 @@ ApplyLayout layout_apply(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_t
     L.f8 = plan_base_fp8(d_out, d_in, batch);
     L.ksplit = L.f8.ksplit;
   } else if (fp4) {
-    if (batch > 0) L.f4 = plan_fp4(d_out, d_in, batch, limbs, base - kBaseFp4);
+    if (batch > 0) L.f4 = plan_fp4(d_out, d_in, batch, limbs, base - kBaseFp4, false);  // fp32 partial sums
   } else if (tc) {
     L.tc = plan_base_tc(d_out, d_in, batch);
     L.ksplit = L.tc.ksplit;

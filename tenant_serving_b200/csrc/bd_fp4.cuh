@@ -126,7 +126,7 @@ struct Fp4Mat {                 // a packed operand: codes, tiled block scales, 
   const float* row;
 };
 constexpr int kFp4LimbsBf16 = 4, kFp4LimbsF32 = 6;
-Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt);
+Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt, bool y_bf16);
 bd_status launch_fp4_limbs(const Fp4Plan& p, int fmt, const void* x, int64_t d_in, int64_t tokens, uint8_t* xc,
                            uint8_t* xs, float* xmul, uint32_t* reset_status, cudaStream_t s);
 bd_status launch_fp4_mm(const Fp4Plan& p, int fmt, const Fp4Mat& w, const Fp4Mat& x, int64_t d_out, int64_t d_in,

@@ -20,8 +20,9 @@
 
 namespace bd {
 
-constexpr int kMmThreads = 128;
+constexpr int kMmThreads = 256;
 constexpr uint32_t kMmABytes = 128 * 128;  // W codes of a stage
+constexpr int kMaxSplit = 8;               // CTAs of a cluster that split K (a power of two)
 
 // D[tmem] (+)= (A * SFA) (B * SFB), 4-bit operands with block scales in tensor memory
 template <int FMT>
@@ -175,6 +176,23 @@ __device__ __forceinline__ void store_y(const MmArgs& p, int64_t t, int64_t row,
     reinterpret_cast<uint16_t*>(p.y)[t * p.d_out + row] = (uint16_t)f2bf_bits(v);
   else
     reinterpret_cast<float*>(p.y)[t * p.d_out + row] = v;
+}
+
+// four consecutive rows of a token
+__device__ __forceinline__ void store_y4(const MmArgs& p, int64_t t, int64_t row, float4 v) {
+  if ((p.d_out & 3) == 0) {
+    if (row >= p.d_out) return;
+    if (p.y_bf16)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.y) + t * p.d_out + row) =
+          make_uint2(f2bf_bits(v.x) | (f2bf_bits(v.y) << 16), f2bf_bits(v.z) | (f2bf_bits(v.w) << 16));
+    else
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.y) + t * p.d_out + row) = v;
+    return;
+  }
+  const float a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (row + q < p.d_out) store_y(p, t, row + q, a[q]);
 }
 
 // ------------------------------------------------------------------------------------
@@ -342,7 +360,7 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
   } else {
     pdl_wait();
     const int64_t t0 = (int64_t)n_blk * p.h;
-    for (int j = threadIdx.x - 64; j < p.h; j += 64) xr[j] = p.x_row && t0 + j < p.tokens ? p.x_row[t0 + j] : 1.f;
+    for (int j = threadIdx.x - 64; j < p.h; j += kMmThreads - 64) xr[j] = p.x_row && t0 + j < p.tokens ? p.x_row[t0 + j] : 1.f;
   }
 
   const bool ok = mbar_wait(done, 0, nullptr);
@@ -361,13 +379,15 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
 
   const int64_t t0 = (int64_t)n_blk * p.h;
   const int n_tok = (int)min((int64_t)p.h, p.tokens - t0);
-  const uint32_t lane_addr = tmem_d + ((uint32_t)(warp * 32) << 16);
+  // eight warps: warps w and w + 4 read the same 32 lanes (rows) and take turns at the groups
+  const int set = warp >> 2, r0 = (warp & 3) * 32 + lane;
+  const uint32_t lane_addr = tmem_d + ((uint32_t)((warp & 3) * 32) << 16);
   constexpr int kTok = Group<L>::kTok;
-  const int64_t row = m_blk * 128 + threadIdx.x;
-  const bool in = row < p.d_out && !aborted;
-  const float rs = in && p.w_row ? p.w_row[row] : 1.f;
   if (split == 1) {
-    for (int c0 = 0; c0 < n_tok; c0 += kTok) {
+    const int64_t row = m_blk * 128 + r0;
+    const bool in = row < p.d_out && !aborted;
+    const float rs = in && p.w_row ? p.w_row[row] : 1.f;
+    for (int c0 = set * kTok; c0 < n_tok; c0 += 2 * kTok) {
       float v[kTok];
       load_group<L>(lane_addr + (uint32_t)(c0 * L), v);
 #pragma unroll
@@ -386,28 +406,47 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
   // (a CTA of this cluster could be waiting for what one of another cluster's holds, and
   // that one for this).
   cluster_wait();
-  for (int c0 = 0; c0 < n_tok; c0 += kTok) {
+  const int log2 = 31 - __clz(split);  // split is a power of two
+  const uint32_t mine = smem_u32(gather + (size_t)rank * share * 128 + r0);
+  for (int c0 = set * kTok; c0 < n_tok; c0 += 2 * kTok) {
     float v[kTok];
     load_group<L>(lane_addr + (uint32_t)(c0 * L), v);
 #pragma unroll
     for (int j = 0; j < kTok; ++j)
       if (c0 + j < n_tok) {
         const int t = c0 + j;
-        st_cluster_f32(map_cluster(smem_u32(gather + ((size_t)rank * share + t / split) * 128 + threadIdx.x),
-                                   (uint32_t)(t % split)),
-                       v[j]);
+        st_cluster_f32(map_cluster(mine + (uint32_t)(t >> log2) * 512, (uint32_t)(t & (split - 1))), v[j]);
       }
   }
   tc_fence_before();  // tensor memory goes back before the barrier, for the same reason
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem_d, tcols);
+  // four rows of a token per lane, a token per warp
+  const int64_t row = m_blk * 128 + 4 * lane;
+  float rs[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) rs[q] = p.w_row && row + q < p.d_out ? p.w_row[row + q] : 1.f;
   cluster_arrive();
   cluster_wait();
-  for (int j = 0; rank + j * split < n_tok; ++j) {
-    float v = 0.f;
-    for (int r = 0; r < split; ++r) v += gather[((size_t)r * share + j) * 128 + threadIdx.x];
+  for (int j = warp; rank + j * split < n_tok; j += kMmThreads / 32) {
+    const float4* g = reinterpret_cast<const float4*>(gather + (size_t)j * 128) + lane;
+    float4 u[kMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+      if (r < split) u[r] = g[(size_t)r * share * 32];
+    float4 v = u[0];
+#pragma unroll
+    for (int r = 1; r < kMaxSplit; ++r)
+      if (r < split) {
+        v.x += u[r].x;
+        v.y += u[r].y;
+        v.z += u[r].z;
+        v.w += u[r].w;
+      }
     const int t = rank + j * split;
-    if (in) store_y(p, t0 + t, row, v * rs * xr[t]);
+    const float xs = xr[t];
+    if (!aborted)
+      store_y4(p, t0 + t, row, make_float4(v.x * rs[0] * xs, v.y * rs[1] * xs, v.z * rs[2] * xs, v.w * rs[3] * xs));
   }
 }
 
@@ -420,9 +459,9 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
 // tensor memory: [0, n_tile) and [n_tile - overlap, ...), so the next tile's MMAs start as
 // soon as the epilogue has read the overlap (the columns that it reads first), and run beside
 // the rest of it.
-constexpr int kPairThreads = 256;       // warp 0 loads, warp 1 MMAs, warps 4-7 epilogue
+constexpr int kPairThreads = 384;       // warp 0 loads, warp 1 MMAs, warps 4-7 and 8-11 epilogue
 constexpr uint32_t kPairSfCol = 448;    // scales in columns 448..511
-constexpr uint32_t kPairOutBytes = 64 * 128 * 4;  // outputs of 64 tokens x 128 rows on their way out
+constexpr uint32_t kPairOut = 2 * 64 * 128;  // outputs on their way out: 64 tokens x 128 rows of each set
 constexpr int kPairGroupM = 8;          // tiles are walked in bands of this many row blocks
 
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
@@ -488,15 +527,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   constexpr uint32_t kStage = kMmABytes + kBBytes + 3 * kSfBytes;
   constexpr uint32_t kSfaCols = kTilesPerStage * 4;
   constexpr int kGroups = kNTile / Group<L>::kCols;
-  constexpr int kFirst = (kOverlap + Group<L>::kCols - 1) / Group<L>::kCols;  // groups that hold the overlap
+  static_assert(kOverlap <= 2 * Group<L>::kCols, "the sets' first groups hold the overlap");
   constexpr int kTok = Group<L>::kTok;
-  constexpr int kOutBufs = 64 / kTok;                        // 2 groups of 32 tokens, or 8 of 8
+  constexpr int kOutBufs = 64 / kTok;                        // of a set: 2 groups of 32 tokens, or 8 of 8
   const int stages = p.stages;
   uint8_t* sa = smem;                                        // [stages] W codes, X codes, scales
   uint8_t* sb = sa + (size_t)stages * kMmABytes;
   uint8_t* ss = sb + (size_t)stages * kBBytes;
-  uint8_t* sy = ss + (size_t)stages * 3 * kSfBytes;          // [kOutBufs] groups of finished outputs
-  uint64_t* full = reinterpret_cast<uint64_t*>(sy + kPairOutBytes);
+  uint8_t* sy = ss + (size_t)stages * 3 * kSfBytes;          // [2 sets][kOutBufs] groups of finished outputs
+  const uint32_t out_bytes = p.y_bf16 ? kPairOut * 2 : kPairOut * 4;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sy + out_bytes);
   uint64_t* empty = full + stages;
   uint64_t* acc_full = empty + stages;  // [2] an accumulator is complete (both CTAs)
   uint64_t* drained = acc_full + 2;     // the overlap of the current tile has been read (even CTA)
@@ -525,7 +565,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     mbar_init(&acc_full[0], 1);
     mbar_init(&acc_full[1], 1);
-    mbar_init(drained, 8);  // four epilogue warps of each CTA
+    mbar_init(drained, 16);  // eight epilogue warps of each CTA
     *abort_flag = 0;
     mbar_fence_init();
     tma_prefetch_desc(&tm_w);
@@ -639,9 +679,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     if (timed_out) *abort_flag = 1;
   } else if (warp >= 4) {
-    const int w = warp - 4;
+    // two sets of four warps take turns at the groups of a tile
+    const int w = warp & 3, set = (warp - 4) >> 2;
     const uint32_t drained_bar = map_cluster(smem_u32(drained), 0);
     const int r0 = w * 32 + lane;  // row of this CTA's half of the tile
+    uint8_t* const bufs = sy + (size_t)set * (out_bytes / 2);
     int j = 0, out = 0;            // tiles and groups so far
     for (int64_t i = pair; i < tiles; i += pairs, ++j) {
       int m, n;
@@ -650,39 +692,39 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const bool in = row < p.d_out;
       const float rs = in && p.w_row ? p.w_row[row] : 1.f;
       const int64_t t0 = (int64_t)n * p.h;
-      float xs = 1.f;  // lane k holds the scale of token g * kTok + k of the next group
-      auto token_scale = [&](int g) {
-        const int64_t t = t0 + (int64_t)g * kTok + lane;
+      // the overlap lies at the end of the even accumulator and at the start of the odd one:
+      // the groups that hold it (one of each set) come first
+      auto group_of = [&](int q) { return (j & 1) ? q : kGroups - 1 - q; };
+      auto token_scale = [&](int q) {  // lane k: the scale of token k of the group
+        const int64_t t = t0 + (int64_t)group_of(q) * kTok + lane;
         return p.x_row && lane < kTok && t < p.tokens ? p.x_row[t] : 1.f;
       };
-      // the overlap lies at the end of the even accumulator and at the start of the odd one
-      auto group_of = [&](int q) { return (j & 1) ? q : kGroups - 1 - q; };
-      xs = token_scale(group_of(0));
+      float xs = set < kGroups ? token_scale(set) : 1.f;
       if (!mbar_wait(&acc_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag)) {
         timed_out = true;
         break;
       }
       tc_fence_after();
       const uint32_t at = tmem + (j & 1 ? kNTile - kOverlap : 0) + ((uint32_t)(w * 32) << 16);
-      for (int q = 0; q < kGroups; ++q) {
+      for (int q = set; q < kGroups; q += 2) {
         const int g = group_of(q);
         const int64_t tg = t0 + (int64_t)g * kTok;
         float v[kTok];
         load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
-        if (q == kFirst - 1) {
+        if (q == set) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(drained_bar);
         }
         const float xg = xs;
-        if (q + 1 < kGroups) xs = token_scale(group_of(q + 1));
+        if (q + 2 < kGroups) xs = token_scale(q + 2);
 #pragma unroll
         for (int c = 0; c < kTok; ++c) v[c] = v[c] * rs * __shfl_sync(0xffffffffu, xg, c);
         if (p.y_tma) {
           // [token][128 rows] in shared memory, then one bulk store of the group; a buffer is
           // written again only after the store that read it (waited for before the barrier
           // that every writer passes)
-          uint8_t* buf = sy + (size_t)(out % kOutBufs) * (kTok * 128 * 4);
+          uint8_t* buf = bufs + (size_t)(out % kOutBufs) * (out_bytes / 2 / kOutBufs);
           if (p.y_bf16) {
 #pragma unroll
             for (int c = 0; c < kTok; ++c)
@@ -693,7 +735,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 2) : "memory");
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");
           if (w == 0 && lane == 0) {
             if (row0 < p.d_out && tg < p.tokens) tma_store_2d(&tm_y, buf, (int)row0, (int)tg);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
@@ -761,7 +803,56 @@ static bool encode_out(CUtensorMap* m, const MmArgs& a, int box_tokens) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt) {
+// K split and stages of k_fp4_mm_rows. For each split the time is estimated in SM cycles as
+// the larger of what an SM has to load (60 bytes per cycle) and its longest chain: 1200 per
+// CTA it starts, and for each set of resident CTAs 1500 until the first data, then per stage
+// the instruction issue or the MMAs, and 1500 for a cluster's join; the best split is taken.
+// Clusters of 4 and 8 do not fit every SM (132 and 120 at one CTA each, by the occupancy
+// query). Stages take the shared memory that the resident CTAs of an SM leave each other.
+// Measured (us, splits 1 / 2 / 4 / 8): 1 token on 4096 x 4096 9.4 / 7.8 / 6.4 / 8.5, 20 tokens
+// fp32 on 4096 x 14336 25.8 / 16.8 / 13.2 / 13.8, 77 4-bit tokens on 1024 x 4096 10.5 / 8.0 /
+// 6.2 / 5.4, 64 tokens on 14336 x 4096 (the product alone) 18.7 / 27.1 / 37.3 / 57.7: the rule
+// takes 4, 4, 8 and 1.
+static void plan_rows(Fp4Plan& p, int sf) {
+  const int sms = sm_count();
+  const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m;
+  const size_t stage = kMmABytes + (size_t)p.n_tile * 128 + (size_t)sf * (1 + (p.n_tile + 127) / 128);
+  const int sf_cols = sf / kFp4TileBytes * 4 * (1 + (p.n_tile + 127) / 128);
+  int tcols = 32;
+  while (tcols < (p.n_tile + 31) / 32 * 32 + 2 * sf_cols) tcols *= 2;
+  const double mma = 4.0 * (p.n_tile / 2 > 48 ? p.n_tile / 2 : 48);
+  const double step = mma > 450 ? mma : 450;
+  double best = 1e30;
+  for (int split = 1; split <= kMaxSplit && split <= p.kblocks; split *= 2) {
+    const size_t gather = split > 1 ? (size_t)split * ((p.h + split - 1) / split) * 512 : 0;
+    const size_t fixed = 1024 + gather + (size_t)p.h * 4 + 17 * 8 + 16;
+    const int need = (p.kblocks + split - 1) / split;
+    const int usable = split <= 2 ? sms : (split == 4 ? sms * 132 / 148 : sms * 120 / 148);
+    const int64_t per_sm = (tiles * split + usable - 1) / usable;
+    // resident CTAs of an SM: all of its share if tensor and shared memory allow
+    int res = (int)(per_sm < 512 / tcols ? per_sm : 512 / tcols);
+    if (res > 6) res = 6;
+    const int two = need < 2 ? need : 2;
+    while (res > 1 && (size_t)res * (fixed + two * stage + 1024) > 227 * 1024) --res;
+    int st = (int)((227 * 1024 / res - 1024 - fixed) / stage);
+    if (st < 1) continue;
+    if (st > need) st = need;
+    if (st > 8) st = 8;
+    const double waves = (double)((per_sm + res - 1) / res);
+    const double load = (double)per_sm * need * stage / 60.0;
+    const double chain = 1200.0 * per_sm + waves * (1500 + need * step + (split > 1 ? 1500 : 0));
+    const double cost = load > chain ? load : chain;
+    if (cost < best) {
+      best = cost;
+      p.split = split;
+      p.stages = st;
+      p.smem = fixed + st * stage;
+      p.ctas = tiles * split;
+    }
+  }
+}
+
+Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt, bool y_bf16) {
   Fp4Plan p = {};
   p.limbs = limbs;
   p.kblocks = (int)((d_in + kFp4KStage - 1) / kFp4KStage);
@@ -777,9 +868,11 @@ Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt
     p.tiles_n = (int)((tokens + p.h - 1) / p.h);
     p.tiles_m = (int)((d_out + 255) / 256);
     const size_t stage = kMmABytes + (size_t)p.n_tile * 64 + 3 * (size_t)sf;
-    p.stages = (int)((226 * 1024 - 1024 - kPairOutBytes) / stage);
+    const size_t out = (size_t)kPairOut * (y_bf16 ? 2 : 4);
+    p.stages = (int)((226 * 1024 - 1024 - out) / stage);
+    if (p.stages > 6) p.stages = 6;
     p.split = 1;
-    p.smem = 1024 + p.stages * stage + kPairOutBytes + (2 * p.stages + 3) * 8 + 16;
+    p.smem = 1024 + p.stages * stage + out + (2 * p.stages + 3) * 8 + 16;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2;
     p.ctas = 2 * (tiles < pairs ? tiles : pairs);
   } else {
@@ -789,19 +882,7 @@ Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt
     p.n_stride = (p.n_tile + 127) / 128 * 128;
     p.tiles_n = (int)((tokens + p.h - 1) / p.h);
     p.tiles_m = (int)((d_out + 127) / 128);
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_m;
-    p.split = 1;
-    while (p.split < 8 && p.split * 2 <= p.kblocks && tiles * p.split < sm_count()) p.split *= 2;
-    const size_t stage = kMmABytes + (size_t)p.n_tile * 128 + (size_t)sf * (1 + (p.n_tile + 127) / 128);
-    const size_t gather = p.split > 1 ? (size_t)p.split * ((p.h + p.split - 1) / p.split) * 512 : 0;
-    const size_t fixed = 1024 + gather + (size_t)p.h * 4 + 17 * 8 + 16;
-    int st = (int)((220 * 1024 - fixed) / stage);
-    const int need = (p.kblocks + p.split - 1) / p.split;
-    if (st > need) st = need;
-    if (st > 8) st = 8;
-    p.stages = st;
-    p.smem = fixed + st * stage;
-    p.ctas = tiles * p.split;
+    plan_rows(p, sf);
   }
   p.x_rows = limbs > 1 ? (int64_t)p.tiles_n * p.n_stride : tokens;
   p.xc_bytes = limbs > 1 ? align_up((size_t)p.x_rows * (size_t)(d_in / 2), 256) : 0;
@@ -914,7 +995,7 @@ struct LinearLayout {
 };
 LinearLayout layout_linear(int64_t d_out, int64_t d_in, int64_t tokens, int32_t y_dtype, int fmt) {
   LinearLayout L;
-  L.p = plan_fp4(d_out, d_in, tokens, y_dtype == BD_F32 ? kFp4LimbsF32 : kFp4LimbsBf16, fmt);
+  L.p = plan_fp4(d_out, d_in, tokens, y_dtype == BD_F32 ? kFp4LimbsF32 : kFp4LimbsBf16, fmt, y_dtype == BD_BF16);
   L.off_c = kStatusBytes;
   L.off_s = L.off_c + L.p.xc_bytes;
   L.off_mul = L.off_s + L.p.xs_bytes;
@@ -941,7 +1022,7 @@ extern "C" bd_status bd_matmul_fp4(const uint8_t* w_codes, const uint8_t* w_scal
   if (st != BD_OK || tokens == 0) return st;
   if (!x_scales) return BD_ERR_NULL;
   if (!aligned16(x_scales) || (reinterpret_cast<uintptr_t>(x_row_scales) & 3u)) return BD_ERR_ALIGN;
-  return launch_fp4_mm(plan_fp4(d_out, d_in, tokens, 1, fmt), fmt, w, x, d_out, d_in, tokens, y, y_dtype,
+  return launch_fp4_mm(plan_fp4(d_out, d_in, tokens, 1, fmt, y_dtype == BD_BF16), fmt, w, x, d_out, d_in, tokens, y, y_dtype,
                        static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(stream));
 }
 
