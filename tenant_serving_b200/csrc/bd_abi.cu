@@ -16,7 +16,8 @@ static const char* const kKernelNames[kKindCount] = {
     "tc_gather",         "delta_tc",     "selftest_wait",
     "quant_fp8",         "x_limbs",      "base_fp8",
     "fp4_quant",         "fp4_dequant",  "fp4_tile_scales",
-    "fp4_limbs",         "fp4_mm",
+    "fp4_limbs",         "fp4_mm",       "fp4_seg_limbs",
+    "delta_fp4",
 };
 
 const char* kernel_name(int32_t kind) {

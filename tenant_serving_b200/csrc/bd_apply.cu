@@ -47,8 +47,8 @@ inline int max_groups_for(int64_t batch, int32_t n_tenants) {
   return (int)((batch + kLutTokens - 1) / kLutTokens + keys);
 }
 
-__device__ __forceinline__ bool tc_eligible(const bd_tenant& T, int64_t d_in) {
-  const bool mode_ok = ((T.mode == BD_SCALE_GROUP || T.mode == BD_SCALE_BLOCK) && T.group_size >= 64 &&
+__device__ __forceinline__ bool tc_eligible(const bd_tenant& T, int64_t d_in, int min_group) {
+  const bool mode_ok = ((T.mode == BD_SCALE_GROUP || T.mode == BD_SCALE_BLOCK) && T.group_size >= min_group &&
                         scale_mode_ok(T.mode, T.group_size, d_in)) ||
                        T.mode == BD_SCALE_ROW || T.mode == BD_SCALE_COL || T.mode == BD_SCALE_TENSOR;
   const bool ptr_ok = T.signs != nullptr && T.scales != nullptr &&
@@ -62,7 +62,8 @@ constexpr int kPlanQ = 3 + kLutClasses;  // tokens, tc segments, gathered X rows
 __global__ void __launch_bounds__(1024) k_tenant_bucket(const int32_t* __restrict__ ids, int batch,
                                                         int n_tenants, int max_groups, int max_tc,
                                                         const bd_tenant* __restrict__ tenants,
-                                                        int tc_min, int64_t d_in, int64_t lut_tiles,
+                                                        int tc_min, int tc_tokens, int tc_group,
+                                                        int64_t d_in, int64_t lut_tiles,
                                                         int split_cap, int lut_ctas,
                                                         int32_t* __restrict__ lut_cnt,
                                                         int32_t* __restrict__ seg_base,
@@ -104,10 +105,10 @@ __global__ void __launch_bounds__(1024) k_tenant_bucket(const int32_t* __restric
     for (int i = 0; i < kPlanQ; ++i) q[i] = 0;
     q[0] = c;
     if (c == 0) return;
-    const bool tc = max_tc > 0 && k < n_tenants && c >= tc_min && tc_eligible(tenants[k], d_in);
+    const bool tc = max_tc > 0 && k < n_tenants && c >= tc_min && tc_eligible(tenants[k], d_in, tc_group);
     if (tc) {
-      q[1] = (c + kTcMaxTokens - 1) / kTcMaxTokens;
-      for (int j = 0; j < c; j += kTcMaxTokens) q[2] += (min(kTcMaxTokens, c - j) + 15) & ~15;
+      q[1] = (c + tc_tokens - 1) / tc_tokens;
+      for (int j = 0; j < c; j += tc_tokens) q[2] += (min(tc_tokens, c - j) + 15) & ~15;
     } else if (k == n_tenants) {
       q[3 + 4] = (c + kLutTokens - 1) / kLutTokens;
     } else {
@@ -175,8 +176,8 @@ __global__ void __launch_bounds__(1024) k_tenant_bucket(const int32_t* __restric
     int q[kPlanQ];
     plan(k, c, q);
     if (q[1] > 0) {
-      for (int j = 0; j < c; j += kTcMaxTokens) {
-        const int n = min(kTcMaxTokens, c - j);
+      for (int j = 0; j < c; j += tc_tokens) {
+        const int n = min(tc_tokens, c - j);
         tc_tenant[tidx] = k;
         tc_rec[tidx] = tenants[k];
         tc_start[tidx] = off + j;
@@ -304,7 +305,7 @@ struct ApplyLayout {
   int ksplit;
   int split_cap;  // lookup units (x K chunks) that may keep partial sums
   int64_t xg_rows;
-  size_t off_seg, off_tcrec, off_part, off_xg, off_xinv, off_x8, off_x4s, off_xmul, off_lpart, off_lcnt, total;
+  size_t off_seg, off_tcrec, off_part, off_xg, off_xinv, off_x8, off_x4s, off_xmul, off_dc, off_ds, off_lpart, off_lcnt, total;
 };
 
 // What the base is held in. kBasePlain: w_dtype's own type; kBaseFp8: e4m3 codes; kBaseFp4 +
@@ -320,14 +321,17 @@ ApplyLayout layout_apply(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_t
   L.max_groups = max_groups_for(batch, n_tenants);
   if (L.max_groups < 1) L.max_groups = 1;
   // a batch smaller than the many-token threshold has no tensor-core segment at all
-  if (tc_delta && batch >= kTcMinTokens) {
+  if (tc_delta && fp4 && n_tenants > 0) {
+    // every tenant in the batch whose record allows it, in segments of fp4_seg_tokens tokens
+    L.max_tc = (int)((batch < n_tenants ? batch : n_tenants) + batch / fp4_seg_tokens(limbs));
+  } else if (tc_delta && !fp4 && batch >= kTcMinTokens) {
     // segments: at most one per many-token tenant plus one per extra kTcSegTokens tokens
     int64_t by_tokens = batch / kTcMinTokens, by_tenants = n_tenants;
     L.max_tc = (int)((by_tokens < by_tenants ? by_tokens : by_tenants) + batch / kTcMaxTokens + 1);
   } else {
     L.max_tc = 0;
   }
-  L.xg_rows = tc_delta ? batch + 15 * (int64_t)L.max_tc : 0;
+  L.xg_rows = tc_delta && !fp4 ? batch + 15 * (int64_t)L.max_tc : 0;
   L.ksplit = 1;
   if (fp8) {
     L.f8 = plan_base_fp8(d_out, d_in, batch);
@@ -355,6 +359,11 @@ ApplyLayout layout_apply(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_t
   off = align_up(off + (fp4 ? L.f4.xs_bytes : 0), 256);
   L.off_xmul = off;
   off = align_up(off + (fp8 ? (size_t)L.f8.xmul_count : fp4 ? (size_t)batch : 0) * sizeof(float), 256);
+  // limbs of the delta segments' tokens over a 4-bit base
+  L.off_dc = off;
+  off = align_up(off + (fp4 ? (size_t)L.max_tc * kFp4SegRows * (d_in / 2) : 0), 256);
+  L.off_ds = off;
+  off = align_up(off + (fp4 ? (size_t)L.max_tc * fp4_tiles_k(d_in, BD_FP4_MX) * kFp4TileBytes : 0), 256);
   // lookup-kernel K split: partial sums [unit][512 rows][4 tokens] and arrival counters
   {
     const int64_t tiles = (d_out + kLutTileRows - 1) / kLutTileRows;
@@ -391,7 +400,7 @@ size_t apply_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int3
   for (int fmt = BD_FP4_NV; fmt <= BD_FP4_MX; ++fmt)
     for (int limbs : {kFp4LimbsBf16, kFp4LimbsF32}) {
       const size_t n =
-          layout_apply(d_out, d_in, batch, n_tenants, true, (d_in % 64) == 0, kBaseFp4 + fmt, limbs).total;
+          layout_apply(d_out, d_in, batch, n_tenants, true, true, kBaseFp4 + fmt, limbs).total;
       if (n > most) most = n;
     }
   return most;
@@ -421,9 +430,9 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
     return BD_ERR_ALIGN;
   const bool tc = w_dtype == BD_BF16;  // with an e4m3 or 4-bit base, w_dtype is the activations' bf16
   // the tensor-core delta path needs bf16 activations, fp16 scales and 64-column stages
-  const bool tc_delta = tc && scale_dtype == BD_F16 && (d_in % 64) == 0;
-  ApplyLayout L = layout_apply(d_out, d_in, batch, n_tenants, tc, tc_delta, base,
-                               y_dtype == BD_F32 ? kFp4LimbsF32 : kFp4LimbsBf16);
+  const bool tc_delta = tc && scale_dtype == BD_F16 && ((d_in % 64) == 0 || fp4);
+  const int limbs = y_dtype == BD_F32 ? kFp4LimbsF32 : kFp4LimbsBf16;  // of the 4-bit products
+  ApplyLayout L = layout_apply(d_out, d_in, batch, n_tenants, tc, tc_delta, base, limbs);
   if (!workspace || ws_bytes < L.total) return BD_ERR_WORKSPACE;
   if (!aligned16(workspace)) return BD_ERR_ALIGN;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -438,7 +447,8 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
     return BD_ERR_CUDA;
   launch_begin(K_TENANT_BUCKET, s);
   BD_CUDA_TRY(launch_pdl(k_tenant_bucket, dim3(1), dim3(1024), bucket_smem, s, tenant_ids, (int)batch, n_tenants,
-                         L.max_groups, L.max_tc, tenants, (int)kTcMinTokens, d_in,
+                         L.max_groups, L.max_tc, tenants, fp4 ? 1 : (int)kTcMinTokens,
+                         fp4 ? fp4_seg_tokens(limbs) : kTcMaxTokens, fp4 ? 128 : 64, d_in,
                          (int64_t)((d_out + kLutTileRows - 1) / kLutTileRows), L.split_cap, sm_count(),
                          reinterpret_cast<int32_t*>(ws + L.off_lcnt), seg,
                          reinterpret_cast<bd_tenant*>(ws + L.off_tcrec), status));
@@ -472,7 +482,13 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
   }
 
   // 3. tensor-core delta for the many-token tenants, fused with the combine
-  if (L.max_tc > 0) {
+  if (L.max_tc > 0 && fp4) {
+    bd_status st = launch_delta_fp4(
+        DeltaFp4Args{reinterpret_cast<const bd_tenant*>(ws + L.off_tcrec), seg, L.max_groups, L.max_tc, x, d_out, d_in,
+                     ws + L.off_dc, ws + L.off_ds, y_part, y, y_dtype == BD_BF16, status},
+        limbs, s);
+    if (st != BD_OK) return st;
+  } else if (L.max_tc > 0) {
     bd_status st = launch_delta_tc(reinterpret_cast<const bd_tenant*>(ws + L.off_tcrec), seg,
                                    L.max_groups, L.max_tc, x, d_out, d_in, batch,
                                    reinterpret_cast<__half*>(ws + L.off_xg), L.xg_rows,

@@ -15,6 +15,8 @@ enum Fp4KernelKind : int32_t {
   K_FP4_TILE_SCALES,           // row-major block scales -> the tiled layout
   K_FP4_LIMBS,                 // activations -> 4-bit limbs with power-of-two block scales
   K_FP4_MM,                    // tcgen05 block-scaled 4-bit product
+  K_FP4_SEG_LIMBS,             // limbs of the delta segments' tokens
+  K_DELTA_FP4,                 // the tenants' deltas as a 4-bit product + combine
   kKindCount                   // all kinds
 };
 
@@ -125,6 +127,24 @@ struct Fp4Mat {                 // a packed operand: codes, tiled block scales, 
   const uint8_t* scales;
   const float* row;
 };
+// The deltas over a 4-bit base (bd_delta_fp4.cu): segments of up to fp4_seg_tokens() tokens of
+// one tenant, from the plan in the apply workspace; xc [max_tc][kFp4SegRows][d_in / 2] codes and
+// xs [max_tc][scale tiles] scales of their activations' limbs.
+constexpr int kFp4SegRows = 32;
+__host__ __device__ constexpr int fp4_seg_tokens(int limbs) { return kFp4SegRows / limbs; }  // 8, or 5
+struct DeltaFp4Args {
+  const bd_tenant* tc_rec;
+  const int32_t* seg;
+  int max_groups, max_tc;
+  const void* x;
+  int64_t d_out, d_in;
+  uint8_t *xc, *xs;
+  const float* y_part;
+  void* y;
+  bool y_bf16;
+  uint32_t* status;
+};
+bd_status launch_delta_fp4(const DeltaFp4Args& a, int limbs, cudaStream_t s);
 constexpr int kFp4LimbsBf16 = 4, kFp4LimbsF32 = 6;
 Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt, bool y_bf16);
 bd_status launch_fp4_limbs(const Fp4Plan& p, int fmt, const void* x, int64_t d_in, int64_t tokens, uint8_t* xc,
