@@ -390,7 +390,11 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
 // the accumulator of its own W rows. Two accumulators overlap by what the scales take of
 // tensor memory: [0, n_tile) and [n_tile - overlap, ...), so the next tile's MMAs start as
 // soon as the epilogue has read the overlap (the columns that it reads first), and run beside
-// the rest of it.
+// the rest of it. At 256 x 256 a stage's loads (39 KB per CTA in BD_FP4_NV) take as long as 64
+// bytes per cycle and SM allow, 610 cycles; its MMAs 512.
+// With few tiles two pairs of a cluster share one (split == 2), half of K each: then each CTA
+// sends the sums of half of its accumulator's groups to its counterpart of the other pair and
+// adds what it is sent to the other half.
 constexpr int kPairThreads = 384;       // warp 0 loads, warp 1 MMAs, warps 4-7 and 8-11 epilogue
 constexpr uint32_t kPairSfCol = 448;    // scales in columns 448..511
 constexpr uint32_t kPairOut = 2 * 64 * 128;  // outputs on their way out: 64 tokens x 128 rows of each set
@@ -426,12 +430,13 @@ __device__ __forceinline__ void umma_fp4_pair(uint32_t d_tmem, uint64_t adesc, u
 __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
-// arrives on the barrier at this offset in both CTAs when the MMAs issued so far are done
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// arrives on the barrier at this offset in both CTAs of a pair (mask: their ranks) when the MMAs
+// issued so far are done
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(mask)
       : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
@@ -442,6 +447,20 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
                "r"(smem_u32(src)), "r"(c0), "r"(c1)
                : "memory");
+}
+
+// whether `v` holds in all 128 threads that meet at named barrier `id`
+__device__ __forceinline__ bool bar_all(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred.aligned q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
 }
 
 template <int FMT, int L>
@@ -476,11 +495,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int cta = (int)cluster_rank();
+  const int rank = (int)cluster_rank(), cta = rank & 1, lead = rank & ~1;
   const bool leader = cta == 0;
+  const uint16_t mask = (uint16_t)(3u << lead);
   const int tiles_m = (int)((p.d_out + 255) / 256);
   const int64_t tiles = (int64_t)tiles_m * p.tiles_n;
-  const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
+  // with a split, cluster `pair` owns tile `pair` and there is no other
+  const int pairs = (int)gridDim.x / (2 * p.split), pair = (int)blockIdx.x / (2 * p.split);
+  const int kb_first = p.split == 2 ? p.kblocks * (rank >> 1) / 2 : 0;
+  const int kb_end = p.split == 2 ? p.kblocks * ((rank >> 1) + 1) / 2 : p.kblocks;
   // tile i of the walk: bands of kPairGroupM row blocks, all N tiles of a band before the next
   auto tile_of = [&](int64_t i, int& m, int& n) {
     const int64_t band = i / ((int64_t)kPairGroupM * p.tiles_n);
@@ -525,14 +548,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     int it = 0, s = 0;  // stages used so far, stage of the ring
     uint32_t ph = 1;    // a fresh barrier's "previous" phase counts as complete
-    const uint32_t full0 = map_cluster(smem_u32(full), 0);
+    const uint32_t full0 = map_cluster(smem_u32(full), lead);
     for (int64_t i = pair; i < tiles && !timed_out; i += pairs) {
       int m, n;
       tile_of(i, m, n);
       const int w_row0 = m * 256 + cta * 128;
       const int x_row0 = n * p.n_stride;
       const int w_tile0 = (w_row0 >> 7) * p.tiles_kw, x_tile0 = (x_row0 >> 7) * p.tiles_kw;
-      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+      for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
         if (!mbar_wait(&empty[s], ph, abort_flag)) {
           timed_out = true;
           break;
@@ -576,7 +599,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
       }
       const uint32_t d = tmem + (j & 1 ? kNTile - kOverlap : 0);
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = kb_first; kb < kb_end; ++kb) {
         if (!mbar_wait(&full[s], ph, abort_flag)) {
           timed_out = true;
           break;
@@ -596,9 +619,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tmem_cp_scales_pair(sfb + 8 * t + 4, sd + ((2 * kSfBytes + t * kFp4TileBytes) >> 4));
               }
               umma_fp4_pair<FMT>(d, ad + 2 * k, bdsc + 2 * k, FMT == BD_FP4_MX && (k & 1) ? id1 : id0, sfa + 4 * t,
-                                 sfb + 8 * t, k > 0 ? 1u : (kb > 0 ? 1u : 0u));
+                                 sfb + 8 * t, k > 0 ? 1u : (kb > kb_first ? 1u : 0u));
             }
-          umma_commit_pair(&empty[s]);
+          umma_commit_pair(&empty[s], mask);
         }
         __syncwarp();
         if (++s == stages) {
@@ -606,33 +629,69 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           ph ^= 1;
         }
       }
-      if (elect_one()) umma_commit_pair(&acc_full[j & 1]);
+      if (elect_one()) umma_commit_pair(&acc_full[j & 1], mask);
       __syncwarp();
     }
     if (timed_out) *abort_flag = 1;
-  } else if (warp >= 4) {
-    // two sets of four warps take turns at the groups of a tile
-    const int w = warp & 3, set = (warp - 4) >> 2;
-    const uint32_t drained_bar = map_cluster(smem_u32(drained), 0);
-    const int r0 = w * 32 + lane;  // row of this CTA's half of the tile
-    uint8_t* const bufs = sy + (size_t)set * (out_bytes / 2);
-    int j = 0, out = 0;            // tiles and groups so far
+  }
+
+  // ---------------- epilogue: two sets of four warps take turns at the groups of a tile ----------------
+  const int w = warp & 3, set = warp >= 8 ? 1 : 0;
+  const int r0 = w * 32 + lane;  // row of this CTA's half of a tile
+  uint8_t* const bufs = sy + (size_t)set * (out_bytes / 2);
+  int out = 0;                   // groups so far
+  // lane k: the scale of token k of group g of the tile at token t0
+  auto token_scale = [&](int64_t t0, int g) {
+    const int64_t t = t0 + (int64_t)g * kTok + lane;
+    return p.x_row && lane < kTok && t < p.tokens ? p.x_row[t] : 1.f;
+  };
+  // outputs of group g: v times the row's scale rs and the tokens' xs
+  auto emit = [&](int64_t row0, int64_t t0, int g, float rs, float xs, float* v) {
+    const int64_t tg = t0 + (int64_t)g * kTok;
+#pragma unroll
+    for (int c = 0; c < kTok; ++c) v[c] = v[c] * rs * __shfl_sync(0xffffffffu, xs, c);
+    if (p.y_tma) {
+      // [token][128 rows] in shared memory, then one bulk store of the group; a buffer is
+      // written again only after the store that read it (waited for before the barrier that
+      // every writer passes)
+      uint8_t* buf = bufs + (size_t)(out % kOutBufs) * (out_bytes / 2 / kOutBufs);
+      if (p.y_bf16) {
+#pragma unroll
+        for (int c = 0; c < kTok; ++c) reinterpret_cast<uint16_t*>(buf)[c * 128 + r0] = (uint16_t)f2bf_bits(v[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kTok; ++c) reinterpret_cast<float*>(buf)[c * 128 + r0] = v[c];
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      if (w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 2) : "memory");
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");
+      if (w == 0 && lane == 0) {
+        if (row0 < p.d_out && tg < p.tokens) tma_store_2d(&tm_y, buf, (int)row0, (int)tg);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+      ++out;
+    } else {
+      const int n_tok = (int)min((int64_t)kTok, p.tokens - tg);
+#pragma unroll
+      for (int c = 0; c < kTok; ++c)
+        if (row0 + r0 < p.d_out && c < n_tok) store_y(p, tg + c, row0 + r0, v[c]);
+    }
+  };
+  if (warp >= 4 && p.split == 1) {
+    const uint32_t drained_bar = map_cluster(smem_u32(drained), lead);
+    int j = 0;  // tiles so far
     for (int64_t i = pair; i < tiles; i += pairs, ++j) {
       int m, n;
       tile_of(i, m, n);
-      const int64_t row0 = (int64_t)m * 256 + cta * 128, row = row0 + r0;
-      const bool in = row < p.d_out;
-      const float rs = in && p.w_row ? p.w_row[row] : 1.f;
-      const int64_t t0 = (int64_t)n * p.h;
+      const int64_t row0 = (int64_t)m * 256 + cta * 128, t0 = (int64_t)n * p.h;
+      const float rs = p.w_row && row0 + r0 < p.d_out ? p.w_row[row0 + r0] : 1.f;
       // the overlap lies at the end of the even accumulator and at the start of the odd one:
       // the groups that hold it (one of each set) come first
       auto group_of = [&](int q) { return (j & 1) ? q : kGroups - 1 - q; };
-      auto token_scale = [&](int q) {  // lane k: the scale of token k of the group
-        const int64_t t = t0 + (int64_t)group_of(q) * kTok + lane;
-        return p.x_row && lane < kTok && t < p.tokens ? p.x_row[t] : 1.f;
-      };
-      float xs = set < kGroups ? token_scale(set) : 1.f;
-      if (!mbar_wait(&acc_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag)) {
+      float xs = set < kGroups ? token_scale(t0, group_of(set)) : 1.f;
+      // (all warps of a set leave together: emit() has a barrier for them)
+      const bool come = mbar_wait(&acc_full[j & 1], (uint32_t)(j >> 1) & 1u, abort_flag);
+      if (!bar_all(1 + set, come)) {
         timed_out = true;
         break;
       }
@@ -640,7 +699,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t at = tmem + (j & 1 ? kNTile - kOverlap : 0) + ((uint32_t)(w * 32) << 16);
       for (int q = set; q < kGroups; q += 2) {
         const int g = group_of(q);
-        const int64_t tg = t0 + (int64_t)g * kTok;
         float v[kTok];
         load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
         if (q == set) {
@@ -649,41 +707,50 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (lane == 0) mbar_arrive_cluster(drained_bar);
         }
         const float xg = xs;
-        if (q + 2 < kGroups) xs = token_scale(q + 2);
-#pragma unroll
-        for (int c = 0; c < kTok; ++c) v[c] = v[c] * rs * __shfl_sync(0xffffffffu, xg, c);
-        if (p.y_tma) {
-          // [token][128 rows] in shared memory, then one bulk store of the group; a buffer is
-          // written again only after the store that read it (waited for before the barrier
-          // that every writer passes)
-          uint8_t* buf = bufs + (size_t)(out % kOutBufs) * (out_bytes / 2 / kOutBufs);
-          if (p.y_bf16) {
-#pragma unroll
-            for (int c = 0; c < kTok; ++c)
-              reinterpret_cast<uint16_t*>(buf)[c * 128 + r0] = (uint16_t)f2bf_bits(v[c]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < kTok; ++c) reinterpret_cast<float*>(buf)[c * 128 + r0] = v[c];
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kOutBufs - 2) : "memory");
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + set) : "memory");
-          if (w == 0 && lane == 0) {
-            if (row0 < p.d_out && tg < p.tokens) tma_store_2d(&tm_y, buf, (int)row0, (int)tg);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-          ++out;
-        } else {
-          const int n_tok = (int)min((int64_t)kTok, p.tokens - tg);
-#pragma unroll
-          for (int c = 0; c < kTok; ++c)
-            if (in && c < n_tok) store_y(p, tg + c, row, v[c]);
-        }
+        if (q + 2 < kGroups) xs = token_scale(t0, group_of(q + 2));
+        emit(row0, t0, g, rs, xg, v);
       }
     }
-    if (p.y_tma && w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (timed_out) *abort_flag = 1;
   }
+  if (p.split == 2) {
+    int m, n;
+    tile_of(pair, m, n);
+    const int64_t row0 = (int64_t)m * 256 + cta * 128, t0 = (int64_t)n * p.h;
+    constexpr int kHalf = (kGroups + 1) / 2;  // groups of the first pair; the others are the second's
+    const int own0 = rank < 2 ? 0 : kHalf, own1 = rank < 2 ? kHalf : kGroups;
+    const int far0 = rank < 2 ? kHalf : 0, far1 = rank < 2 ? kGroups : kHalf;
+    const uint32_t at = tmem + ((uint32_t)(w * 32) << 16);
+    float* sums = reinterpret_cast<float*>(smem);  // [token][128 rows], in the W stages
+    if (warp >= 4 && !mbar_wait(&acc_full[0], 0, abort_flag)) *abort_flag = 1;
+    tc_fence_after();
+    __syncwarp();
+    cluster_arrive();  // all MMAs and loads of the cluster are over: the stages are free
+    cluster_wait();
+    if (warp >= 4)
+      for (int g = far0 + set; g < far1; g += 2) {
+        float v[kTok];
+        load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
+        const uint32_t to = map_cluster(smem_u32(sums + (g - far0) * kTok * 128 + r0), (uint32_t)(rank ^ 2));
+#pragma unroll
+        for (int c = 0; c < kTok; ++c) st_cluster_f32(to + c * 512, v[c]);
+      }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp >= 4) {
+      const float rs = p.w_row && row0 + r0 < p.d_out ? p.w_row[row0 + r0] : 1.f;
+      for (int g = own0 + set; g < own1; g += 2) {
+        const float xs = token_scale(t0, g);
+        float v[kTok];
+        load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
+#pragma unroll
+        for (int c = 0; c < kTok; ++c) v[c] += sums[((g - own0) * kTok + c) * 128 + r0];
+        emit(row0, t0, g, rs, xs, v);
+      }
+    }
+  }
+  if (warp >= 4 && p.y_tma && w == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -791,10 +858,12 @@ Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt
     const size_t out = (size_t)kPairOut * (y_bf16 ? 2 : 4);
     p.stages = (int)((226 * 1024 - 1024 - out) / stage);
     if (p.stages > 6) p.stages = 6;
-    p.split = 1;
+    // two pairs per tile when all tiles then still run at once, unless K is short
+    const int64_t all = (int64_t)p.tiles_m * p.tiles_n;
+    p.split = all * 4 <= sm_count() * 132 / 148 && p.kblocks >= 8 ? 2 : 1;
     p.smem = 1024 + p.stages * stage + out + (2 * p.stages + 3) * 8 + 16;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2;
-    p.ctas = 2 * (tiles < pairs ? tiles : pairs);
+    p.ctas = p.split == 2 ? 4 * tiles : 2 * (tiles < pairs ? tiles : pairs);
   } else {
     p.h = (int)((tokens + step - 1) / step * step);
     if (p.h > 128) p.h = 128;  // a cluster keeps h * 128 sums in each CTA's shared memory
@@ -826,7 +895,7 @@ bd_status launch_mm(const Fp4Plan& p, const Fp4Mat& w, const Fp4Mat& x, const Mm
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)(p.pair ? 2 : p.split);
+  attr[1].val.clusterDim.x = (unsigned)(p.pair ? 2 * p.split : p.split);
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
