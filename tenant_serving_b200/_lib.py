@@ -428,57 +428,56 @@ def bd_apply_multi_fp8(w_codes, w_scales, table, tenant_ids, x, y=None, y_dtype=
 
 
 # The 4-bit calls below are also made for single tokens, where the host's time per call counts:
-# they read tensor properties once and pass plain integers.
+# they read each tensor property once, keep what they look up, and pass plain integers.
 _FP4_BLOCK = {BD_FP4_NV: 16, BD_FP4_MX: 32}
+_FP4 = {}  # torch, its dtypes' codes and the entry points, filled on first use
 
 
-class _Current:
-    """Makes another device than the current one current for a call."""
-
-    def __init__(self, index):
-        self._ctx = _torch().cuda.device(index)
-
-    def __enter__(self):
-        self._ctx.__enter__()
-
-    def __exit__(self, *exc):
-        self._ctx.__exit__(*exc)
+def _fp4_env():
+    torch = _torch()
+    _FP4["torch"], _FP4["u8"], _FP4["f32"], _FP4["bf16"] = torch, torch.uint8, torch.float32, torch.bfloat16
+    _FP4["code"] = {torch.float32: BD_F32, torch.bfloat16: BD_BF16, torch.float16: BD_F16}
+    _FP4["device"] = torch.cuda.current_device
+    _FP4["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return _FP4
 
 
 def _on_device(ts):
     """Index of the GPU that holds all of a call's tensors (None entries aside)."""
-    dev = -1
+    dev = None
     for t in ts:
         if t is not None:
             d = t.get_device()
-            if d < 0:
-                raise ValueError("tensors passed to the library must live on the GPU")
-            if d != dev and dev >= 0:
-                raise ValueError("the tensors of a call live on one GPU")
-            dev = d
+            if d != dev:
+                if d < 0:
+                    raise ValueError("tensors passed to the library must live on the GPU")
+                if dev is not None:
+                    raise ValueError("the tensors of a call live on one GPU")
+                dev = d
     return dev
 
 
-def _raw_stream(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream
-    torch = _torch()
-    try:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    except AttributeError:
-        return torch.cuda.current_stream(dev).cuda_stream
+def _fp4_code(t):
+    env = _FP4 or _fp4_env()
+    code = env["code"].get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _fp4_call(name, dev, args, stream):
     """Calls an entry point with its device current and that device's stream as last argument."""
-    torch = _torch()
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
-        rc = fn(*args, _raw_stream(stream, dev))
+    env = _FP4 or _fp4_env()
+    fn = env.get(name)
+    if fn is None:
+        fn = env[name] = getattr(lib(), name)
+    if env["device"]() == dev:
+        rc = fn(*args, env["stream"](dev) if stream is None else stream.cuda_stream)
     else:
-        with _Current(dev):
-            rc = fn(*args, _raw_stream(stream, dev))
-    if rc != BD_OK:
+        with env["torch"].cuda.device(dev):
+            rc = fn(*args, env["stream"](dev) if stream is None else stream.cuda_stream)
+    if rc:
         raise BitDeltaError(rc, name)
 
 
@@ -515,20 +514,26 @@ def fp4_workspace(nbytes, device):
 
 def _fp4_shape(codes, scales, row_scales, fmt, where):
     """[rows, cols] of a packed matrix, its buffers' sizes and types checked."""
-    torch = _torch()
-    if fmt not in _FP4_BLOCK:
+    env = _FP4 or _fp4_env()
+    block = _FP4_BLOCK.get(fmt)
+    if block is None:
         raise BitDeltaError(BD_ERR_CONFIG, where)
-    u8 = torch.uint8
-    if codes.dtype is not u8 or scales.dtype is not u8 or (row_scales is not None and row_scales.dtype is not torch.float32):
+    u8 = env["u8"]
+    if codes.dtype is not u8 or scales.dtype is not u8:
         raise TypeError(f"{where}: codes and scales are uint8, row scales float32")
-    if not (codes.is_contiguous() and scales.is_contiguous()) or (row_scales is not None and not row_scales.is_contiguous()):
-        raise ValueError(f"{where}: packed matrices are contiguous")
     rows, half = codes.shape
     cols = 2 * half
-    per = 4 * _FP4_BLOCK[fmt]
-    if rows < 1 or cols < 32 or cols % 32 or scales.numel() != -(-rows // 128) * -(-cols // per) * 512 or \
-            (row_scales is not None and row_scales.numel() != rows):
+    if rows < 1 or cols < 32 or cols % 32 or scales.numel() != -(-rows // 128) * -(-cols // (4 * block)) * 512:
         raise BitDeltaError(BD_ERR_SHAPE, where)
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{where}: packed matrices are contiguous")
+    if row_scales is not None:
+        if row_scales.dtype is not env["f32"]:
+            raise TypeError(f"{where}: codes and scales are uint8, row scales float32")
+        if row_scales.numel() != rows:
+            raise BitDeltaError(BD_ERR_SHAPE, where)
+        if not row_scales.is_contiguous():
+            raise ValueError(f"{where}: packed matrices are contiguous")
     return rows, cols
 
 
@@ -536,7 +541,7 @@ def _fp4_out(y, rows, cols, dtype, like, where):
     if y is None:
         torch = _torch()
         return torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=like.device)
-    if y.dim() != 2 or y.size(0) != rows or y.size(1) != cols or not y.is_contiguous():
+    if y.shape != (rows, cols) or not y.is_contiguous():
         raise BitDeltaError(BD_ERR_SHAPE, where)
     return y
 
@@ -574,8 +579,8 @@ def bd_quantize_fp4(x, fmt, codes=None, scales=None, row_scales=None, hat=None, 
         raise BitDeltaError(BD_ERR_SHAPE, where)
     if hat is not None or hat_dtype is not None:
         hat = _fp4_out(hat, rows, cols, hat_dtype, x, where)
-    _fp4_call(where, dev, (_p(x), dtype_code(x), rows, cols, x.stride(0) if rows > 1 else cols, fmt, _p(codes),
-                           _p(scales), _p(row_scales), _p(hat), dtype_code(hat) if hat is not None else BD_F32), stream)
+    _fp4_call(where, dev, (_p(x), _fp4_code(x), rows, cols, x.stride(0) if rows > 1 else cols, fmt, _p(codes),
+                           _p(scales), _p(row_scales), _p(hat), _fp4_code(hat) if hat is not None else BD_F32), stream)
     return codes, scales, row_scales, hat
 
 
@@ -585,7 +590,7 @@ def bd_dequantize_fp4(codes, scales, row_scales, fmt, out=None, out_dtype=None, 
     dev = _on_device((codes, scales, row_scales, out))
     rows, cols = _fp4_shape(codes, scales, row_scales, fmt, where)
     out = _fp4_out(out, rows, cols, out_dtype, codes, where)
-    _fp4_call(where, dev, (_p(codes), _p(scales), _p(row_scales), fmt, rows, cols, _p(out), dtype_code(out)), stream)
+    _fp4_call(where, dev, (_p(codes), _p(scales), _p(row_scales), fmt, rows, cols, _p(out), _fp4_code(out)), stream)
     return out
 
 
@@ -607,7 +612,7 @@ def bd_matmul_fp4(w_codes, w_scales, w_row, x_codes, x_scales, x_row, fmt, y=Non
     if workspace is None:
         workspace = fp4_workspace(bd_matmul_fp4_workspace_size(d_out, d_in, tokens), w_codes.device)
     _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), _p(x_codes), _p(x_scales), _p(x_row), fmt, d_out,
-                           d_in, tokens, _p(y), dtype_code(y), _p(workspace), workspace.nbytes), stream)
+                           d_in, tokens, _p(y), _fp4_code(y), _p(workspace), workspace.nbytes), stream)
     return y, workspace
 
 
@@ -616,11 +621,12 @@ def bd_linear_fp4_workspace_size(d_out, d_in, tokens) -> int:
 
 
 def _bf16_rows(x, d_in, where):
-    if x.dtype is not _torch().bfloat16:
+    if x.dtype is not (_FP4 or _fp4_env())["bf16"]:
         raise TypeError(f"{where}: activations are bfloat16")
-    if x.dim() != 2 or x.size(1) != d_in or not x.is_contiguous():
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != d_in or not x.is_contiguous():
         raise BitDeltaError(BD_ERR_SHAPE, where)
-    return x.size(0)
+    return shape[0]
 
 
 def bd_linear_fp4(w_codes, w_scales, w_row, x, fmt, y=None, y_dtype=None, workspace=None, stream=None):
@@ -634,7 +640,7 @@ def bd_linear_fp4(w_codes, w_scales, w_row, x, fmt, y=None, y_dtype=None, worksp
         torch = _torch()
         workspace = torch.empty(bd_linear_fp4_workspace_size(d_out, d_in, tokens), dtype=torch.uint8, device=x.device)
     _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), fmt, d_out, d_in, _p(x), tokens, _p(y),
-                           dtype_code(y), _p(workspace), workspace.nbytes), stream)
+                           _fp4_code(y), _p(workspace), workspace.nbytes), stream)
     return y, workspace
 
 
@@ -659,7 +665,7 @@ def bd_apply_multi_fp4(w_codes, w_scales, w_row, table, tenant_ids, x, fmt, y=No
         workspace = torch.empty(max(bd_apply_fp4_workspace_size(d_out, d_in, batch, table.n), 16),
                                 dtype=torch.uint8, device=x.device)
     _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), fmt, d_out, d_in, tab, table.n, table.scale_dtype,
-                           _p(tenant_ids), _p(x), batch, _p(y), dtype_code(y), _p(workspace), workspace.nbytes),
+                           _p(tenant_ids), _p(x), batch, _p(y), _fp4_code(y), _p(workspace), workspace.nbytes),
               stream)
     return y, workspace
 
