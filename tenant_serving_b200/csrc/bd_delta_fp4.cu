@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       const uint8_t* signs = reinterpret_cast<const uint8_t*>(T.signs) + (int64_t)(row0 / 512) * nst * 16384 + (row0 % 512) * 32;
       const uint8_t* scales = static_cast<const uint8_t*>(T.scales) + (int64_t)(row0 / 512) * nst * 2048 + (row0 % 512) * 4;
       for (int st = 0; st < nst; ++st) {
-        if (!mbar_wait(&raw_empty[rs], rph, abort_flag)) {
+        if (!warp_wait(&raw_empty[rs], rph, abort_flag)) {
           ok = false;
           break;
         }
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
     if (!ok) {  // every copy lands before the shared memory goes away
       *abort_flag = 1;
       for (int64_t i = n > kDfRaw ? n - kDfRaw : 0; i < n; ++i)
-        mbar_wait(&raw_full[i % kDfRaw], (uint32_t)(i / kDfRaw) & 1u, nullptr);
+        warp_wait(&raw_full[i % kDfRaw], (uint32_t)(i / kDfRaw) & 1u, nullptr);
     }
   } else if (warp == 2) {
     // ---------------- limbs ----------------
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       it.next();
       if (it.left > 0) count = sg.count[it.seg];
       for (int st = 0; st < nst; ++st) {
-        if (!mbar_wait(&done[s], ph, abort_flag)) {
+        if (!warp_wait(&done[s], ph, abort_flag)) {
           ok = false;
           break;
         }
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       // at: they get the time instead
       *abort_flag = 1;
       for (int64_t i = n > kDfStages ? n - kDfStages : 0; i < n; ++i)
-        mbar_wait(&full[i % kDfStages], (uint32_t)(i / kDfStages) & 1u, nullptr, 2000000);
+        warp_wait(&full[i % kDfStages], (uint32_t)(i / kDfStages) & 1u, nullptr, 2000000);
     }
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
@@ -394,11 +394,11 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       const uint32_t step = chunked ? kDfN : 0;  // from a chunk's accumulator to the next one's
       const uint32_t on = chunked ? 0u : 1u;     // a second chunk adds to the first one's
       for (int st = 0; st < nst; ++st) {
-        if ((chunked || st == 0) && bn >= 2 && !mbar_wait(&bank_empty[bn & 1], ((bn >> 1) & 1) ^ 1u, abort_flag)) {
+        if ((chunked || st == 0) && bn >= 2 && !warp_wait(&bank_empty[bn & 1], ((bn >> 1) & 1) ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
-        if (!mbar_wait(&full[s], ph, abort_flag)) {
+        if (!warp_wait(&full[s], ph, abort_flag)) {
           ok = false;
           break;
         }
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
     // no MMA may be in flight when the CTA leaves
     if (elect_one()) umma_commit(drain);
     __syncwarp();
-    mbar_wait(drain, 0, nullptr);
+    warp_wait(drain, 0, nullptr);
   } else if (warp >= 4 && warp < 12) {
     // ---------------- signs -> E2M1 in tensor memory, every other stage ----------------
     const int r = (warp & 3) * 32 + lane;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       };
       for (int st = 0; st < nst; ++st, turn = !turn) {
         if (turn) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&raw_full[rs], rph, abort_flag))) {
+          if (!warp_wait(&raw_full[rs], rph, abort_flag)) {
             ok = false;
             break;
           }
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&raw_empty[rs]);
-          if (!__all_sync(0xffffffffu, mbar_wait(&done[s], ph, abort_flag))) {
+          if (!warp_wait(&done[s], ph, abort_flag)) {
             ok = false;
             break;
           }
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       const int seg = it.seg;
       const int32_t mode = tc_rec[seg].mode, count = sg.count[seg], start = sg.start[seg];
       const int my_tok = lane < count ? sg.perm[start + lane] : 0;
-      if (!__all_sync(0xffffffffu, mbar_wait(&item_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag))) {
+      if (!warp_wait(&item_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag)) {
         ok = false;
         break;
       }
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
     int slot = 0;
     for (; it.left > 0 && ok; it.next(), ++n) {
       const DfItem& I = items[n & 1];
-      if (!__all_sync(0xffffffffu, mbar_wait(&item_full[n & 1], (n >> 1) & 1, abort_flag))) {
+      if (!warp_wait(&item_full[n & 1], (n >> 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kDfThreads, 1)
       for (int j = 0; j < kTok; ++j) acc[0][j] = acc[1][j] = 0.f;
       const int banks = chunked ? nst : 1;
       for (int k = 0; k < banks; ++k, ++bn) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&bank_full[bn & 1], (bn >> 1) & 1, abort_flag))) {
+        if (!warp_wait(&bank_full[bn & 1], (bn >> 1) & 1, abort_flag)) {
           ok = false;
           break;
         }

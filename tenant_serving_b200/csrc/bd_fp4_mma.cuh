@@ -46,6 +46,12 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0;
 }
+// A bounded wait of a whole warp: all lanes give up when one does, so that what the warp does
+// together afterwards stays together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
+                                          long long limit_cycles = kWaitCycles) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit_cycles));
+}
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
 
 // N (8, 16 or 32) consecutive 32-bit columns of the thread's lane; tmem_wait() before use

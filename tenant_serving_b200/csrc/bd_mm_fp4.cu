@@ -192,107 +192,108 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
 
   bool timed_out = false;
   if (warp == 0) {
-      const int64_t x_row0 = (int64_t)n_blk * p.n_stride;
-      const int xt0 = (int)(x_row0 >> 7);
-      const int xt = min(sfb_tiles, p.x_row_tiles - xt0);
-      auto sf_of = [&](int i) {
-        return (uint32_t)min(kTilesPerStage, p.tiles_kw - (kb0 + i) * kTilesPerStage) * kFp4TileBytes;
-      };
-      auto load_w = [&](int i) {
-        const int s = i % stages;
-        const uint32_t sf = sf_of(i);
-        mbar_arrive_expect_tx(&full[s], kMmABytes + b_bytes + sf * (1 + xt));
-        tma_load_2d(sa + (size_t)s * kMmABytes, &tm_w, &full[s], (kb0 + i) * 128, (int)(m_blk * 128));
-        bulk_load(ssa + (size_t)s * kSfBytes,
-                  p.w_scales + (m_blk * p.tiles_kw + (int64_t)(kb0 + i) * kTilesPerStage) * kFp4TileBytes, sf, &full[s]);
-      };
-      // the weights of the first stages are asked for before the kernel that writes X is over
-      const int first = min(nkb, stages);
-      int early = 0;
-      if (p.w_early) {
-        if (elect_one())
-          for (int i = 0; i < first; ++i) load_w(i);
-        __syncwarp();
-        early = first;
-      }
-      pdl_wait();
-      pdl_trigger();
-      int issued = 0;
-      for (int i = 0; i < nkb; ++i) {
-        const int s = i % stages;
-        const uint32_t ph = (uint32_t)(i / stages) & 1u;
-        if (i >= stages && !mbar_wait(&empty[s], ph ^ 1u, abort_flag)) {
-          timed_out = true;
-          *abort_flag = 1;
-          break;
-        }
-        if (elect_one()) {
-          if (i >= early) load_w(i);
-          const uint32_t sf = sf_of(i);
-          tma_load_2d(sb + (size_t)s * b_bytes, &tm_x, &full[s], (kb0 + i) * 128, (int)x_row0);
-          for (int j = 0; j < xt; ++j)
-            bulk_load(
-                ssb + ((size_t)s * sfb_tiles + j) * kSfBytes,
-                p.x_scales + ((int64_t)(xt0 + j) * p.tiles_kw + (int64_t)(kb0 + i) * kTilesPerStage) * kFp4TileBytes,
-                sf, &full[s]);
-        }
-        __syncwarp();
-        ++issued;
-      }
-      if (lane == 0) *issued_out = issued;
-  } else if (warp == 1) {
-      // Everything that a stage needs is a constant step from the stage before: the issuing
-      // thread has 512 cycles of MMAs per stage to hide its own work behind.
-      const uint32_t id0 = umma_idesc_fp4(128, p.n_tile, FMT == BD_FP4_MX, 0);
-      const uint32_t id1 = umma_idesc_fp4(128, p.n_tile, FMT == BD_FP4_MX, 2);
-      const uint64_t ad0 = umma_desc_sw128(smem_u32(sa)), bd0 = umma_desc_sw128(smem_u32(sb));
-      const uint64_t sad0 = scale_desc(smem_u32(ssa)), sbd0 = scale_desc(smem_u32(ssb));
-      const uint32_t b_step = b_bytes >> 4, sb_step = (uint32_t)sfb_tiles * (kSfBytes >> 4);
-      const bool two = sfb_tiles == 2;
-      int s = 0;
-      uint32_t ph = 0;
-      for (int i = 0; i < nkb; ++i) {
-        if (!mbar_wait(&full[s], ph, abort_flag)) {
-          timed_out = true;
-          *abort_flag = 1;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t sfa = tmem_d + d_cols + (uint32_t)(i & 1) * sf_cols;
-          const uint32_t sfb = sfa + kSfaCols;
-          const uint64_t ad = ad0 + (uint32_t)s * (kMmABytes >> 4), bdsc = bd0 + (uint32_t)s * b_step;
-          const uint64_t sad = sad0 + (uint32_t)s * (kSfBytes >> 4), sbd = sbd0 + (uint32_t)s * sb_step;
-          const int steps = p.k_steps - (kb0 + i) * 4;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps) {
-              // scales: SFA tile of a step in 4 columns, SFB likewise per 128 rows
-              const int t = FMT == BD_FP4_NV ? k : k >> 1;
-              const uint32_t sfb_t = sfb + (two ? 8 : 4) * t;
-              if (FMT == BD_FP4_NV || (k & 1) == 0) {
-                tmem_cp_scales(sfa + 4 * t, sad + t * (kFp4TileBytes >> 4));
-                tmem_cp_scales(sfb_t, sbd + t * (kFp4TileBytes >> 4));
-                if (two) tmem_cp_scales(sfb_t + 4, sbd + (kSfBytes >> 4) + t * (kFp4TileBytes >> 4));
-              }
-              // 64 columns: 32 bytes further inside the swizzled 128-byte row
-              umma_fp4<FMT>(tmem_d, ad + 2 * k, bdsc + 2 * k, FMT == BD_FP4_MX && (k & 1) ? id1 : id0, sfa + 4 * t,
-                            sfb_t, k > 0 ? 1u : (i > 0 ? 1u : 0u));
-            }
-          umma_commit(&empty[s]);
-        }
-        __syncwarp();
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1;
-        }
-      }
-      if (elect_one()) umma_commit(done);
+    const int64_t x_row0 = (int64_t)n_blk * p.n_stride;
+    const int xt0 = (int)(x_row0 >> 7);
+    const int xt = min(sfb_tiles, p.x_row_tiles - xt0);
+    auto sf_of = [&](int i) {
+      return (uint32_t)min(kTilesPerStage, p.tiles_kw - (kb0 + i) * kTilesPerStage) * kFp4TileBytes;
+    };
+    auto load_w = [&](int i) {
+      const int s = i % stages;
+      const uint32_t sf = sf_of(i);
+      mbar_arrive_expect_tx(&full[s], kMmABytes + b_bytes + sf * (1 + xt));
+      tma_load_2d(sa + (size_t)s * kMmABytes, &tm_w, &full[s], (kb0 + i) * 128, (int)(m_blk * 128));
+      bulk_load(ssa + (size_t)s * kSfBytes,
+                p.w_scales + (m_blk * p.tiles_kw + (int64_t)(kb0 + i) * kTilesPerStage) * kFp4TileBytes, sf, &full[s]);
+    };
+    // the weights of the first stages are asked for before the kernel that writes X is over
+    const int first = min(nkb, stages);
+    int early = 0;
+    if (p.w_early) {
+      if (elect_one())
+        for (int i = 0; i < first; ++i) load_w(i);
       __syncwarp();
+      early = first;
+    }
+    pdl_wait();
+    pdl_trigger();
+    int issued = 0;
+    for (int i = 0; i < nkb; ++i) {
+      const int s = i % stages;
+      const uint32_t ph = (uint32_t)(i / stages) & 1u;
+      if (i >= stages && !warp_wait(&empty[s], ph ^ 1u, abort_flag)) {
+        timed_out = true;
+        *abort_flag = 1;
+        break;
+      }
+      if (elect_one()) {
+        if (i >= early) load_w(i);
+        const uint32_t sf = sf_of(i);
+        tma_load_2d(sb + (size_t)s * b_bytes, &tm_x, &full[s], (kb0 + i) * 128, (int)x_row0);
+        for (int j = 0; j < xt; ++j)
+          bulk_load(
+              ssb + ((size_t)s * sfb_tiles + j) * kSfBytes,
+              p.x_scales + ((int64_t)(xt0 + j) * p.tiles_kw + (int64_t)(kb0 + i) * kTilesPerStage) * kFp4TileBytes,
+              sf, &full[s]);
+      }
+      __syncwarp();
+      ++issued;
+    }
+    if (lane == 0) *issued_out = issued;
+  } else if (warp == 1) {
+    // Everything that a stage needs is a constant step from the stage before: the issuing
+    // thread has 512 cycles of MMAs per stage to hide its own work behind.
+    const uint32_t id0 = umma_idesc_fp4(128, p.n_tile, FMT == BD_FP4_MX, 0);
+    const uint32_t id1 = umma_idesc_fp4(128, p.n_tile, FMT == BD_FP4_MX, 2);
+    const uint64_t ad0 = umma_desc_sw128(smem_u32(sa)), bd0 = umma_desc_sw128(smem_u32(sb));
+    const uint64_t sad0 = scale_desc(smem_u32(ssa)), sbd0 = scale_desc(smem_u32(ssb));
+    const uint32_t b_step = b_bytes >> 4, sb_step = (uint32_t)sfb_tiles * (kSfBytes >> 4);
+    const bool two = sfb_tiles == 2;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nkb; ++i) {
+      if (!warp_wait(&full[s], ph, abort_flag)) {
+        timed_out = true;
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sfa = tmem_d + d_cols + (uint32_t)(i & 1) * sf_cols;
+        const uint32_t sfb = sfa + kSfaCols;
+        const uint64_t ad = ad0 + (uint32_t)s * (kMmABytes >> 4), bdsc = bd0 + (uint32_t)s * b_step;
+        const uint64_t sad = sad0 + (uint32_t)s * (kSfBytes >> 4), sbd = sbd0 + (uint32_t)s * sb_step;
+        const int steps = p.k_steps - (kb0 + i) * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < steps) {
+            // scales: SFA tile of a step in 4 columns, SFB likewise per 128 rows
+            const int t = FMT == BD_FP4_NV ? k : k >> 1;
+            const uint32_t sfb_t = sfb + (two ? 8 : 4) * t;
+            if (FMT == BD_FP4_NV || (k & 1) == 0) {
+              tmem_cp_scales(sfa + 4 * t, sad + t * (kFp4TileBytes >> 4));
+              tmem_cp_scales(sfb_t, sbd + t * (kFp4TileBytes >> 4));
+              if (two) tmem_cp_scales(sfb_t + 4, sbd + (kSfBytes >> 4) + t * (kFp4TileBytes >> 4));
+            }
+            // 64 columns: 32 bytes further inside the swizzled 128-byte row
+            umma_fp4<FMT>(tmem_d, ad + 2 * k, bdsc + 2 * k, FMT == BD_FP4_MX && (k & 1) ? id1 : id0, sfa + 4 * t,
+                          sfb_t, k > 0 ? 1u : (i > 0 ? 1u : 0u));
+          }
+        umma_commit(&empty[s]);
+      }
+      __syncwarp();
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1;
+      }
+    }
+    if (elect_one()) umma_commit(done);
+    __syncwarp();
   } else {
     pdl_wait();
     const int64_t t0 = (int64_t)n_blk * p.h;
-    for (int j = threadIdx.x - 64; j < p.h; j += kMmThreads - 64) xr[j] = p.x_row && t0 + j < p.tokens ? p.x_row[t0 + j] : 1.f;
+    for (int j = threadIdx.x - 64; j < p.h; j += kMmThreads - 64)
+      xr[j] = p.x_row && t0 + j < p.tokens ? p.x_row[t0 + j] : 1.f;
   }
 
   const bool ok = mbar_wait(done, 0, nullptr);
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int x_row0 = n * p.n_stride;
       const int w_tile0 = (w_row0 >> 7) * p.tiles_kw, x_tile0 = (x_row0 >> 7) * p.tiles_kw;
       for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
-        if (!mbar_wait(&empty[s], ph, abort_flag)) {
+        if (!warp_wait(&empty[s], ph, abort_flag)) {
           timed_out = true;
           break;
         }
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     // all MMAs that read this CTA's shared memory are over before it leaves (bounded)
     for (int k = max(0, it - stages); k < it; ++k)
-      if (!mbar_wait(&empty[k % stages], (uint32_t)(k / stages) & 1u, abort_flag)) timed_out = true;
+      if (!warp_wait(&empty[k % stages], (uint32_t)(k / stages) & 1u, abort_flag)) timed_out = true;
     if (timed_out) *abort_flag = 1;
   } else if (warp == 1 && leader) {
     const uint32_t id0 = umma_idesc_fp4(256, kNTile, FMT == BD_FP4_MX, 0);
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t ph = 0;
     for (int64_t i = pair; i < tiles && !timed_out; i += pairs, ++j) {
       if (j > 0) {
-        if (!mbar_wait(drained, (uint32_t)(j - 1) & 1u, abort_flag)) {
+        if (!warp_wait(drained, (uint32_t)(j - 1) & 1u, abort_flag)) {
           timed_out = true;
           break;
         }
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       const uint32_t d = tmem + (j & 1 ? kNTile - kOverlap : 0);
       for (int kb = kb_first; kb < kb_end; ++kb) {
-        if (!mbar_wait(&full[s], ph, abort_flag)) {
+        if (!warp_wait(&full[s], ph, abort_flag)) {
           timed_out = true;
           break;
         }
@@ -754,7 +755,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, BD_DEV_TIMEOUT);
+  if (threadIdx.x == 0 && *abort_flag) {
+    atomicOr(p.status, BD_DEV_TIMEOUT);
+    // copies in flight complete on barriers that nobody may wait for any more: they get a
+    // millisecond to land before the shared memory goes away
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000) {
+    }
+  }
+  __syncthreads();
   cluster_arrive();  // neither CTA leaves while the other's MMAs or barriers may reach it
   cluster_wait();
   if (warp == 1)

@@ -294,6 +294,131 @@ def test_apply_matches_oracle(bd, fmt, d_out, d_in, B, counts):
     assert_apply_close(host(y32), y_ref, per_token=True)
 
 
+def _delta_limit(tenants, ids, x, out):
+    """Delta_hat x and its allowed error: limbs as for bf16 activations (blocks of 32; COL scales
+    are multiplied into the activations first), fp32 sums over chunks of 8 or more columns, and
+    two units in the last place for the scales' products."""
+    d_out, d_in = tenants[0]["signs"].shape[0], x.shape[1]
+    y, lim = np.zeros((len(x), d_out)), np.zeros((len(x), d_out))
+    eps = 2.0 ** -16 if out == "f32" else 2.0 ** -10
+    deltas = [O.reconstruct(t["signs"], t["scales"].astype(np.float64), t["mode"], t["group_size"], d_out, d_in)
+              for t in tenants]
+    for t, u in enumerate(ids):
+        if u < 0:
+            continue
+        ten, d = tenants[u], deltas[u]
+        ax = np.abs(x[t]) * (np.asarray(ten["scales"], dtype=np.float64) if ten["mode"] == 2 else 1.0)
+        ad = np.ones_like(d) if ten["mode"] == 2 else np.abs(d)
+        top = ax.reshape(-1, 32).max(1).repeat(32)
+        y[t] = d @ x[t]
+        lim[t] = ad @ (eps * top + 2.0 ** -126) + ((d_in / 8 + 16) * 2.0 ** -23 + 2.0 ** -22) * (ad @ ax)
+    return y, lim
+
+
+MODES = [(0, 128), (0, 256), (0, 32), (1, 0), (2, 0), (3, 0), (4, 128), (4, 512), (4, 64)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("d_out,d_in", [(300, 512), (520, 1536), (129, 2560)])
+def test_deltas_of_every_kind(bd, fmt, out, d_out, d_in):
+    """Every scale mode, group sizes that the 4-bit product takes and that it leaves to the lookup
+    kernel, row-major records beside tiled ones, and 1 to 33 tokens of a tenant in a batch."""
+    import torch
+    rng = np.random.default_rng(d_out + d_in)
+    tenants = [random_tenant(rng, d_out, d_in, m, g or 128) for m, g in MODES] + [random_tenant(rng, d_out, d_in, 0, 128)]
+    for t in tenants:  # larger than in use: the delta is what is held to its bound here
+        t["scales"] = (t["scales"].astype(np.float32) * 40).astype(np.float16)
+    counts = [3, 2, 1, 9, 8, 33, 5, 17, 4, 6]
+    ids = np.concatenate([np.full(c, u) for u, c in enumerate(counts)] + [np.full(7, -1)]).astype(np.int32)
+    rng.shuffle(ids)
+    recs = []
+    for u, t in enumerate(tenants):
+        sg, sc = dev(t["signs"]), dev(t["scales"])
+        if u < len(MODES):
+            sg, sc = bd.bd_prepare_tenant(sg, sc, t["mode"], t["group_size"], d_out, d_in)
+        recs.append((sg, sc, t["mode"], t["group_size"], bd.BD_LAYOUT_TILED if u < len(MODES) else bd.BD_LAYOUT_ROWMAJOR))
+    w, wh = _packed(bd, rng, d_out, d_in, fmt)
+    x = O.decode(activations(rng, len(ids), d_in), "bf16") * 2.0 ** rng.integers(-20, 20, size=(len(ids), 1))
+    x[:, ::31] *= 32
+    xb = bf16_bits(x)
+    x = O.decode(xb, "bf16")
+    y, ws = bd.bd_apply_multi_fp4(*w, bd.TenantTable(recs, "cuda"), dev(ids), dev(xb), fmt,
+                                  y_dtype=torch.float32 if out == "f32" else torch.bfloat16)
+    assert bd.bd_get_status(ws) == (bd.BD_OK, 0)
+    yb, lb = _limit(O.dequantize_fp4(*wh, fmt), x, fmt, "f32", True)
+    if out == "bf16":  # four limbs
+        e = np.abs(x).reshape(len(x), -1, O.fp4_block(fmt)).max(2).repeat(O.fp4_block(fmt), 1) * 2.0 ** -10
+        lb = lb + e @ np.abs(O.dequantize_fp4(*wh, fmt)).T
+    yd, ld = _delta_limit(tenants, ids, x, out)
+    ref, lim = yb + yd, lb + ld + 2.0 ** -23 * (np.abs(yb) + np.abs(yd))
+    _check(y, ref, lim + (2.0 ** -8 * (np.abs(ref) + lim) if out == "bf16" else 0))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_apply_status_and_limits(bd, fmt):
+    """An id out of range and a bad record are reported, their tokens get the base; infinities
+    and NaN stay with their token; no tenants at all; one token of one tenant."""
+    import torch
+    rng = np.random.default_rng(31)
+    d_out, d_in = 200, 512
+    w, wh = _packed(bd, rng, d_out, d_in, fmt)
+    ten = [random_tenant(rng, d_out, d_in, 0, 128) for _ in range(2)]
+    table = _table(bd, ten)
+    xb = activations(rng, 6, d_in)
+    base, _ = bd.bd_linear_fp4(*w, dev(xb), fmt, y_dtype=torch.float32)
+    ids = np.array([0, 7, -1, 1, -5, 0], dtype=np.int32)
+    y, ws = bd.bd_apply_multi_fp4(*w, table, dev(ids), dev(xb), fmt, y_dtype=torch.float32)
+    assert bd.bd_get_status(ws) == (bd.BD_ERR_TENANT_RANGE, bd.BD_DEV_TENANT_RANGE)
+    assert torch.equal(y[[1, 2, 4]], base[[1, 2, 4]]) and not torch.equal(y[0], base[0])
+    bad = bd.TenantTable([(dev(ten[0]["signs"]), dev(ten[0]["scales"]), 0, 96, 1)], "cuda")
+    y, ws = bd.bd_apply_multi_fp4(*w, bad, dev(np.zeros(6, dtype=np.int32)), dev(xb), fmt, y_dtype=torch.float32)
+    assert bd.bd_get_status(ws)[0] == bd.BD_ERR_TENANT_RECORD and torch.equal(y, base)
+    y, ws = bd.bd_apply_multi_fp4(*w, bd.TenantTable([], "cuda"), dev(np.full(6, -1, dtype=np.int32)), dev(xb), fmt,
+                                  y_dtype=torch.float32)
+    assert bd.bd_get_status(ws) == (bd.BD_OK, 0) and torch.equal(y, base)
+    xn = xb.copy()
+    xn[0, 5], xn[3, 300] = 0x7F80, 0x7FC0
+    ids = np.array([0, 0, -1, 1, 1, 0], dtype=np.int32)
+    y, _ = bd.bd_apply_multi_fp4(*w, table, dev(ids), dev(xn), fmt, y_dtype=torch.float32)
+    clean, _ = bd.bd_apply_multi_fp4(*w, table, dev(ids), dev(xb), fmt, y_dtype=torch.float32)
+    assert torch.isnan(y[[0, 3]]).all() and torch.equal(y[[1, 2, 4, 5]], clean[[1, 2, 4, 5]])
+    one, _ = bd.bd_apply_multi_fp4(*w, table, dev(ids[:1]), dev(xb[:1]), fmt, y_dtype=torch.float32)
+    assert_apply_close(host(one), host(clean)[:1].astype(np.float64), tol=1e-6, per_token=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_back_to_back(bd, fmt):
+    """Quantise, product and apply right behind one another on one stream, with new weights each
+    time in the same buffers: every product sees the weights that were written before it."""
+    import torch
+    rng = np.random.default_rng(41)
+    d_out, d_in = 1024, 2048
+    xb = dev(activations(rng, 3, d_in))
+    ws_ = [dev(bf16_bits(rng.normal(0, 0.02, size=(d_out, d_in)))) for _ in range(3)]
+    bufs = bd.fp4_buffers(d_out, d_in, fmt, "cuda")
+    table = _table(bd, [random_tenant(rng, d_out, d_in, 1)])
+    ids = dev(np.array([0, -1, 0], dtype=np.int32))
+    work = bd.fp4_workspace(bd.bd_linear_fp4_workspace_size(d_out, d_in, 3), "cuda")
+    work_a = bd.fp4_workspace(bd.bd_apply_fp4_workspace_size(d_out, d_in, 3, 1), "cuda")
+
+    def one(w):
+        bd.bd_quantize_fp4(w, fmt, *bufs)
+        y, _ = bd.bd_linear_fp4(*bufs, xb, fmt, workspace=work)
+        z, _ = bd.bd_apply_multi_fp4(*bufs, table, ids, xb, fmt, workspace=work_a)
+        return y, z
+
+    want = []
+    for w in ws_:
+        r = one(w)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in r])
+    got = [one(ws_[i % 3]) for i in range(30)]
+    torch.cuda.synchronize()
+    for i, r in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(r, want[i % 3]))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_compress_against_the_served_base_and_serve(bd, fmt):
     """Quantise a base, take a fine-tune's delta against what is served, serve the tenant
@@ -334,19 +459,24 @@ def test_graphs_and_streams(bd, fmt):
     rng = np.random.default_rng(5)
     w, _ = _packed(bd, rng, 1100, 1056, fmt)
     xs = [dev(activations(rng, 24, 1056)) for _ in range(3)]
+    table = _table(bd, [random_tenant(rng, 1100, 1056, m, 32) for m in (1, 2, 0)])
+    ids = dev(rng.integers(-1, 3, size=24).astype(np.int32))
 
     def chain(x, bufs):
         bd.bd_quantize_fp4(x, fmt, *bufs["q"])
         bd.bd_matmul_fp4(*w, *bufs["q"], fmt, y=bufs["y4"], workspace=bufs["ws4"])
         bd.bd_linear_fp4(*w, x, fmt, y=bufs["y"], workspace=bufs["ws"])
-        return bufs["y4"], bufs["y"]
+        bd.bd_apply_multi_fp4(*w, table, ids, x, fmt, y=bufs["ya"], workspace=bufs["wsa"])
+        return bufs["y4"], bufs["y"], bufs["ya"]
 
     def buffers():
         return {"q": bd.fp4_buffers(24, 1056, fmt, "cuda"),
                 "y4": torch.empty((24, 1100), dtype=torch.bfloat16, device="cuda"),
                 "y": torch.empty((24, 1100), dtype=torch.float32, device="cuda"),
                 "ws4": bd.fp4_workspace(bd.bd_matmul_fp4_workspace_size(1100, 1056, 24), "cuda"),
-                "ws": bd.fp4_workspace(bd.bd_linear_fp4_workspace_size(1100, 1056, 24), "cuda")}
+                "ws": bd.fp4_workspace(bd.bd_linear_fp4_workspace_size(1100, 1056, 24), "cuda"),
+                "ya": torch.empty((24, 1100), dtype=torch.bfloat16, device="cuda"),
+                "wsa": bd.fp4_workspace(bd.bd_apply_fp4_workspace_size(1100, 1056, 24, 3), "cuda")}
 
     want = [[t.clone() for t in chain(x, buffers())] for x in xs]
     shared = buffers()
@@ -361,10 +491,10 @@ def test_graphs_and_streams(bd, fmt):
         graphs.append(g)
     for i, w_ in ((0, want[0]), (1, want[1]), (0, want[0])):
         graphs[i].replay()
-        assert all(torch.equal(a, b) for a, b in zip((shared["y4"], shared["y"]), w_))
+        assert all(torch.equal(a, b) for a, b in zip((shared["y4"], shared["y"], shared["ya"]), w_))
     own_x.copy_(xs[2])
     graphs[0].replay()
-    assert all(torch.equal(a, b) for a, b in zip((shared["y4"], shared["y"]), want[2]))
+    assert all(torch.equal(a, b) for a, b in zip((shared["y4"], shared["y"], shared["ya"]), want[2]))
 
     streams = [torch.cuda.Stream() for _ in range(2)]
     bufs = [buffers() for _ in streams]
@@ -375,7 +505,7 @@ def test_graphs_and_streams(bd, fmt):
                 chain(x, b)
     torch.cuda.synchronize()
     for b, w_ in zip(bufs, want):
-        assert all(torch.equal(p, q) for p, q in zip((b["y4"], b["y"]), w_))
+        assert all(torch.equal(p, q) for p, q in zip((b["y4"], b["y"], b["ya"]), w_))
 
 
 def test_wrapper_refusals(bd):
