@@ -38,7 +38,8 @@ constexpr int kMaxBatch = 65536;
 // base-only groups, so that the lookup kernel meets one kind of group for long stretches.
 // Workspace layout (int32): the kSegHeader words, grp_tenant[max_groups],
 // grp_start[max_groups], grp_len[max_groups], tc_tenant[max_tc], tc_start[max_tc],
-// tc_count[max_tc], tc_xrow[max_tc] (first row in the gathered X), perm[batch]; and, in a
+// tc_count[max_tc], tc_xrow[max_tc] (first row in the gathered X; over a 4-bit base, [0] is the
+// number of base-only tokens, which then have no groups), perm[batch]; and, in a
 // region of its own, a copy of each tensor-core segment's tenant record.
 constexpr int kTcMaxTokens = kTcSegTokens;
 
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(1024) k_tenant_bucket(const int32_t* __restric
                                                         int n_tenants, int max_groups, int max_tc,
                                                         const bd_tenant* __restrict__ tenants,
                                                         int tc_min, int tc_tokens, int tc_group,
+                                                        bool fp4,
                                                         int64_t d_in, int64_t lut_tiles,
                                                         int split_cap, int lut_ctas,
                                                         int32_t* __restrict__ lut_cnt,
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(1024) k_tenant_bucket(const int32_t* __restric
       q[1] = (c + tc_tokens - 1) / tc_tokens;
       for (int j = 0; j < c; j += tc_tokens) q[2] += (min(tc_tokens, c - j) + 15) & ~15;
     } else if (k == n_tenants) {
-      q[3 + 4] = (c + kLutTokens - 1) / kLutTokens;
+      if (!(fp4 && max_tc > 0)) q[3 + 4] = (c + kLutTokens - 1) / kLutTokens;
     } else {
       q[3 + 0] = c / kLutTokens;
       const int rem = c % kLutTokens;
@@ -182,10 +184,12 @@ __global__ void __launch_bounds__(1024) k_tenant_bucket(const int32_t* __restric
         tc_rec[tidx] = tenants[k];
         tc_start[tidx] = off + j;
         tc_count[tidx] = n;
-        tc_xrow[tidx] = xrow;
+        if (!fp4) tc_xrow[tidx] = xrow;
         xrow += (n + 15) & ~15;
         ++tidx;
       }
+    } else if (fp4 && max_tc > 0 && k == n_tenants) {
+      tc_xrow[0] = c;  // the base-only tokens, last in perm (there is no gathered X)
     } else {
       for (int j = 0; j < c; j += kLutTokens) {
         const int len = min(kLutTokens, c - j);
@@ -448,7 +452,7 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
   launch_begin(K_TENANT_BUCKET, s);
   BD_CUDA_TRY(launch_pdl(k_tenant_bucket, dim3(1), dim3(1024), bucket_smem, s, tenant_ids, (int)batch, n_tenants,
                          L.max_groups, L.max_tc, tenants, fp4 ? 1 : (int)kTcMinTokens,
-                         fp4 ? fp4_seg_tokens(limbs) : kTcMaxTokens, fp4 ? 128 : 64, d_in,
+                         fp4 ? fp4_seg_tokens(limbs) : kTcMaxTokens, fp4 ? 128 : 64, fp4, d_in,
                          (int64_t)((d_out + kLutTileRows - 1) / kLutTileRows), L.split_cap, sm_count(),
                          reinterpret_cast<int32_t*>(ws + L.off_lcnt), seg,
                          reinterpret_cast<bd_tenant*>(ws + L.off_tcrec), status));
@@ -485,7 +489,7 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
   if (L.max_tc > 0 && fp4) {
     bd_status st = launch_delta_fp4(
         DeltaFp4Args{reinterpret_cast<const bd_tenant*>(ws + L.off_tcrec), seg, L.max_groups, L.max_tc, x, d_out, d_in,
-                     ws + L.off_dc, ws + L.off_ds, y_part, y, y_dtype == BD_BF16, status},
+                     ws + L.off_dc, ws + L.off_ds, y_part, y, y_dtype == BD_BF16, status, batch},
         limbs, s);
     if (st != BD_OK) return st;
   } else if (L.max_tc > 0) {

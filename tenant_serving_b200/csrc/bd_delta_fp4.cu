@@ -37,6 +37,7 @@ constexpr uint32_t kDfN = kFp4SegRows;       // MMA N, and X rows of a segment's
 constexpr uint32_t kDfSmallN = 16;           // MMA N of a segment of 1 or 2 tokens
 constexpr uint32_t kDfXBytes = kDfN * 128;
 constexpr uint32_t kDfXsBytes = 2 * kFp4TileBytes;
+constexpr int kDfCopy = 2048;                // columns of y that a block copies at a time
 // tensor memory: two banks of accumulators [2 products][2 chunks], the A ring, scales of one,
 // scales of X
 constexpr uint32_t kDfBank = 4 * kDfN;
@@ -46,14 +47,15 @@ constexpr uint32_t kDfSfb = kDfSfa + 4;
 static_assert(kDfSfb + 8 * kDfStages <= 512, "");
 
 struct DfSegs {
-  const int32_t *start, *count, *perm;
+  const int32_t *start, *count, *base_only, *perm;  // *base_only: tokens of the base alone, last in perm
 };
 __device__ __forceinline__ DfSegs df_segs(const int32_t* seg_base, int max_groups, int max_tc) {
   DfSegs g;
   const int32_t* tenant = seg_base + kSegHeader + 3 * max_groups;
   g.start = tenant + max_tc;
   g.count = g.start + max_tc;
-  g.perm = g.count + 2 * max_tc;
+  g.base_only = g.count + max_tc;
+  g.perm = g.base_only + max_tc;
   return g;
 }
 // The CTA's items in turn: item blockIdx.x + i gridDim.x is (segment, row tile), stepped
@@ -85,17 +87,49 @@ __device__ __forceinline__ bool df_chunked(int32_t mode) { return mode == BD_SCA
 // limbs of a segment's tokens, columns in the signs' order: position 8 j + i of every 32 is
 // column 4 i + j. Limb l of token t of a segment is row l * gs + t of its slot of 32 rows, gs =
 // 2 for a segment of 1 or 2 tokens, else the most tokens a segment has (8, or 5 with 6 limbs).
+// The blocks behind the segments' write y for the tokens of the base alone.
 // ------------------------------------------------------------------------------------
 template <int L>
 __global__ void __launch_bounds__(128) k_fp4_seg_limbs(const int32_t* __restrict__ seg_base, int max_groups,
                                                        int max_tc, const bd_tenant* __restrict__ tc_rec,
                                                        const uint16_t* __restrict__ x, int64_t d_in,
-                                                       uint8_t* __restrict__ xc, uint8_t* __restrict__ xs) {
+                                                       uint8_t* __restrict__ xc, uint8_t* __restrict__ xs,
+                                                       const float* __restrict__ y_part, int64_t d_out, int batch,
+                                                       void* __restrict__ y, bool y_bf16) {
   pdl_wait();  // inputs may come from the previous kernel on the stream
   pdl_trigger();
-  const int seg = blockIdx.x, j = blockIdx.y;
-  if (seg >= seg_base[1]) return;
+  constexpr int kTok = fp4_seg_tokens(L);
   const DfSegs sg = df_segs(seg_base, max_groups, max_tc);
+  if ((int)blockIdx.x >= max_tc * kTok) {
+    const int n = *sg.base_only, chunks = (int)((d_out + kDfCopy - 1) / kDfCopy);
+    const int64_t units = (int64_t)n * chunks, stride = gridDim.x - max_tc * kTok;
+    for (int64_t u = (int64_t)blockIdx.x - max_tc * kTok; u < units; u += stride) {
+      const int64_t c0 = (u % chunks) * kDfCopy, t = sg.perm[batch - n + (int)(u / chunks)];
+      const int64_t c1 = min(c0 + kDfCopy, d_out);
+      const float* p = y_part + t * d_out;
+      if (d_out % 4 == 0) {
+        for (int64_t c = c0 + threadIdx.x * 4; c < c1; c += 512) {
+          const float4 v = *reinterpret_cast<const float4*>(p + c);
+          if (y_bf16)
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(y) + t * d_out + c) =
+                make_uint2(f2bf_bits(v.x) | ((uint32_t)f2bf_bits(v.y) << 16),
+                           f2bf_bits(v.z) | ((uint32_t)f2bf_bits(v.w) << 16));
+          else
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + t * d_out + c) = v;
+        }
+      } else {
+        for (int64_t c = c0 + threadIdx.x; c < c1; c += 128) {
+          if (y_bf16)
+            reinterpret_cast<uint16_t*>(y)[t * d_out + c] = (uint16_t)f2bf_bits(p[c]);
+          else
+            reinterpret_cast<float*>(y)[t * d_out + c] = p[c];
+        }
+      }
+    }
+    return;
+  }
+  const int seg = (int)blockIdx.x / kTok, j = (int)blockIdx.x - seg * kTok;
+  if (seg >= seg_base[1]) return;
   const int count = sg.count[seg];
   if (j >= count) return;
   const int gs = count <= 2 ? 2 : fp4_seg_tokens(L);
@@ -370,41 +404,41 @@ __global__ void __launch_bounds__(kDfThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMAs ----------------
-    const uint32_t sfa = tmem + kDfSfa;
-    if (elect_one()) tmem_cp_scales(sfa, scale_desc(smem_u32(ones)));
-    __syncwarp();
-    const uint64_t bd0 = umma_desc_sw128(smem_u32(sx)), sd0 = scale_desc(smem_u32(sxs));
-    const int k_steps = (int)((d_in + 63) / 64);
-    int s = 0;
-    uint32_t ph = 0, bn = 0;  // ring position; accumulator banks handed to the epilogue so far
-    int32_t mode = 0, count = 0;
-    if (it.left > 0) {
-      mode = tc_rec[it.seg].mode;
-      count = sg.count[it.seg];
-    }
-    while (it.left > 0 && ok) {
-      const bool chunked = df_chunked(mode);
-      const uint32_t nn = count <= 2 ? kDfSmallN : kDfN;
-      it.next();
+    // (one thread walks the stages: it has no vote to take after each wait)
+    if (elect_one()) {
+      const uint32_t sfa = tmem + kDfSfa;
+      tmem_cp_scales(sfa, scale_desc(smem_u32(ones)));
+      const uint64_t bd0 = umma_desc_sw128(smem_u32(sx)), sd0 = scale_desc(smem_u32(sxs));
+      const int k_steps = (int)((d_in + 63) / 64);
+      int s = 0;
+      uint32_t ph = 0, bn = 0;  // ring position; accumulator banks handed to the epilogue so far
+      int32_t mode = 0, count = 0;
       if (it.left > 0) {
         mode = tc_rec[it.seg].mode;
         count = sg.count[it.seg];
       }
-      const uint32_t id0 = umma_idesc_fp4(128, nn, true, 0), id1 = umma_idesc_fp4(128, nn, true, 2);
-      const uint32_t step = chunked ? kDfN : 0;  // from a chunk's accumulator to the next one's
-      const uint32_t on = chunked ? 0u : 1u;     // a second chunk adds to the first one's
-      for (int st = 0; st < nst; ++st) {
-        if ((chunked || st == 0) && bn >= 2 && !warp_wait(&bank_empty[bn & 1], ((bn >> 1) & 1) ^ 1u, abort_flag)) {
-          ok = false;
-          break;
+      while (it.left > 0 && ok) {
+        const bool chunked = df_chunked(mode);
+        const uint32_t nn = count <= 2 ? kDfSmallN : kDfN;
+        it.next();
+        if (it.left > 0) {
+          mode = tc_rec[it.seg].mode;
+          count = sg.count[it.seg];
         }
-        if (!warp_wait(&full[s], ph, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const bool last = chunked || st == nst - 1;
-        if (elect_one()) {
+        const uint32_t id0 = umma_idesc_fp4(128, nn, true, 0), id1 = umma_idesc_fp4(128, nn, true, 2);
+        const uint32_t step = chunked ? kDfN : 0;  // from a chunk's accumulator to the next one's
+        const uint32_t on = chunked ? 0u : 1u;     // a second chunk adds to the first one's
+        for (int st = 0; st < nst; ++st) {
+          if ((chunked || st == 0) && bn >= 2 && !mbar_wait(&bank_empty[bn & 1], ((bn >> 1) & 1) ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait(&full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool last = chunked || st == nst - 1;
           const uint32_t d = tmem + (bn & 1) * kDfBank, d2 = d + step;
           const uint32_t a = tmem + kDfA + 64 * s, sfb = tmem + kDfSfb + 8 * s;
           const uint64_t b = bd0 + (uint32_t)s * (kDfXBytes >> 4), sd = sd0 + (uint32_t)s * (kDfXsBytes >> 4);
@@ -428,21 +462,21 @@ __global__ void __launch_bounds__(kDfThreads, 1)
             umma_mxf4_ts(d2 + 2 * kDfN, a + 56, b + 6, id1, sfa, sfb + 4, 1u);
           }
           umma_commit(&done[s]);
-          if (last) umma_commit(&bank_full[bn & 1]);
-        }
-        __syncwarp();
-        if (last) ++bn;
-        if (++s == kDfStages) {
-          s = 0;
-          ph ^= 1;
+          if (last) {
+            umma_commit(&bank_full[bn & 1]);
+            ++bn;
+          }
+          if (++s == kDfStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
+      if (!ok) *abort_flag = 1;
+      umma_commit(drain);
     }
-    if (!ok) *abort_flag = 1;
-    // no MMA may be in flight when the CTA leaves
-    if (elect_one()) umma_commit(drain);
     __syncwarp();
-    warp_wait(drain, 0, nullptr);
+    warp_wait(drain, 0, nullptr);  // no MMA may be in flight when the CTA leaves
   } else if (warp >= 4 && warp < 12) {
     // ---------------- signs -> E2M1 in tensor memory, every other stage ----------------
     const int r = (warp & 3) * 32 + lane;
@@ -653,9 +687,12 @@ __global__ void __launch_bounds__(kDfThreads, 1)
 // ------------------------------------------------------------------------------------
 template <int L>
 static bd_status launch_delta(const DeltaFp4Args& a, cudaStream_t s) {
+  const int64_t copies = a.batch * ((a.d_out + kDfCopy - 1) / kDfCopy), copy_cap = (int64_t)sm_count() * 4;
+  const int64_t blocks = (int64_t)a.max_tc * fp4_seg_tokens(L) + (copies < copy_cap ? copies : copy_cap);
   launch_begin(K_FP4_SEG_LIMBS, s);
-  BD_CUDA_TRY(launch_pdl(k_fp4_seg_limbs<L>, dim3((unsigned)a.max_tc, fp4_seg_tokens(L)), dim3(128), 0, s, a.seg,
-                         a.max_groups, a.max_tc, a.tc_rec, static_cast<const uint16_t*>(a.x), a.d_in, a.xc, a.xs));
+  BD_CUDA_TRY(launch_pdl(k_fp4_seg_limbs<L>, dim3((unsigned)blocks), dim3(128), 0, s, a.seg, a.max_groups, a.max_tc,
+                         a.tc_rec, static_cast<const uint16_t*>(a.x), a.d_in, a.xc, a.xs, a.y_part, a.d_out,
+                         (int)a.batch, a.y, a.y_bf16));
   launch_end(K_FP4_SEG_LIMBS, s);
   BD_LAUNCH_CHECK();
   CUtensorMap small, full;

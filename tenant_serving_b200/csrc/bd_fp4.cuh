@@ -143,6 +143,7 @@ struct DeltaFp4Args {
   void* y;
   bool y_bf16;
   uint32_t* status;
+  int64_t batch;
 };
 bd_status launch_delta_fp4(const DeltaFp4Args& a, int limbs, cudaStream_t s);
 constexpr int kFp4LimbsBf16 = 4, kFp4LimbsF32 = 6;
