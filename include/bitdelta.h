@@ -497,6 +497,13 @@ bd_status bd_linear_fp4(const uint8_t* w_codes, const uint8_t* w_scales, const f
  *     y[t] = W_hat x[t] + Delta_hat_{u(t)} x[t].
  * Same tenants, ids, output and status rules as bd_apply_multi; x is bf16 [batch][d_in]; the
  * base product is that of bd_linear_fp4 for the same y_dtype.
+ *   Tenants in BD_LAYOUT_TILED with fp16 scales, of the modes ROW, COL and TENSOR or GROUP and
+ *   BLOCK with group_size >= 128, have their deltas multiplied on the tensor cores as 4-bit
+ *   products too, for any number of tokens: x[t] in the limbs of bd_linear_fp4 over blocks of
+ *   32 columns (4 limbs for a BD_BF16 y, 6 for BD_F32, so an element carries at most m * 2^-10
+ *   or m * 2^-16, m its block's largest magnitude; COL scales are first multiplied into x[t]
+ *   in fp32), fp32 sums, scales applied in fp32. The others take the sign-lookup kernel, as
+ *   few-token tenants do in bd_apply_multi.
  *   workspace : bd_apply_fp4_workspace_size() bytes, 16-byte aligned. */
 size_t bd_apply_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t batch, int32_t n_tenants);
 bd_status bd_apply_multi_fp4(const uint8_t* w_codes, const uint8_t* w_scales,

@@ -10,14 +10,18 @@
 //                    every other tenant's tokens, and the base-only ones, are cut into
 //                    lookup groups of <= 4 for k_delta_lut. Invalid ids set a status bit
 //                    and join the base-only tokens. No host synchronisation.
-//   base product     bf16: tcgen05 tensor-core GEMM (bd_base_tc.cu), fp32: k_base_gemv.
-//                    Both write fp32 partial sums y_part[kz][t][row].
+//   base product     bf16: tcgen05 tensor-core GEMM (bd_base_tc.cu), fp32: k_base_gemv,
+//                    e4m3: bd_base_fp8.cu, 4-bit: bd_mm_fp4.cu. All write fp32 partial sums
+//                    y_part[kz][t][row].
 //   k_delta_tc       (bd_delta_tc.cu) the many-token tenants' delta as a tcgen05
 //                    contraction with the +/-s matrix expanded into tensor memory.
 //   k_delta_lut      (bd_delta_lut.cu) the few-token tenants' delta through per-chunk
 //                    sign lookup tables in shared memory, all tokens of a group served by
 //                    one pass over the tenant's bits.
-//   Both delta kernels add the base partial sums in a fixed order and write y (bf16 or
+//   k_delta_fp4      (bd_delta_fp4.cu) over a 4-bit base, every tenant whose record it supports,
+//                    in segments of up to 8 tokens (5 for fp32 y); its limbs kernel writes y
+//                    for the base-only tokens.
+//   The delta kernels add the base partial sums in a fixed order and write y (bf16 or
 //   fp32) in request order.
 #include "bd_fp4.cuh"
 #include "bd_internal.cuh"

@@ -16,6 +16,15 @@
 // columns or more: each 128-column chunk has accumulators of its own, which the epilogue
 // scales and adds in fp32. ROW, TENSOR and COL deltas (COL scales are in the limbs) accumulate
 // over the row.
+//
+// What bounds it: a stage takes about 830 cycles (GROUP) or 740 (ROW), shared between the
+// expansion's instructions and the stage's chain of barriers; the MMAs themselves are cheap
+// (issued twice over they add 2%), HBM is at 36%. 64 one-token tenants on 14336 x 4096 take
+// 180 us where the lookup kernel takes 225 (528 MB of signs and scales: floor 81). A call with
+// 32 ROW tenants and 256 tokens on 6144 x 4096 takes 95 us, with the lookup and fp16
+// tensor-core kernels 228. An item has 256 rows because a stage's barriers are paid per item
+// row block. Without effect or slower: a deeper ring of limbs, a stage's codes made before the
+// wait for its slot, a second MMA warp, two sets of sum warps, shifts on the multiplier.
 #include "bd_fp4_mma.cuh"
 
 namespace bd {

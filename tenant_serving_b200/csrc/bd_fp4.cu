@@ -4,6 +4,10 @@
 // "BitDelta Guide", "3. Quantized Base Model Compatibility (BitDelta + GPTQ / QuIP#)": the
 // 1-bit delta goes on top of quantized base weights; "Per-Axis Weight Deltas for Frequent
 // Model Updates", Future Directions: INT4/FP8 co-design.
+//
+// All of these move bytes: they are bound by HBM from a few MB on, and by their launch below
+// that. Times quoted here and below are of one B200 whose device-to-device copy runs at 6550
+// GB/s, inputs not in L2.
 #include "bd_fp4.cuh"
 
 namespace bd {
@@ -186,7 +190,10 @@ __device__ __forceinline__ uint2 encode16_pow2(const float* v, bool bad, float u
 // ------------------------------------------------------------------------------------
 // quantise, BD_FP4_NV: one CTA per row. A thread holds NB blocks of the row as stored between
 // the row's maximum and the codes, so the row is read once (from memory again in the loop
-// when it has more than 8 blocks per thread).
+// when it has more than 8 blocks per thread). The two reads of a row cannot be closer than the
+// row's maximum; a CTA per row keeps them a barrier apart, and up to 16 rows per SM hide it.
+// Bound by HBM: 28672 x 4096 bf16 with x_hat, 536 MB, in 86-96 us (a plain read of the row
+// twice, one warp per row, took 179).
 // ------------------------------------------------------------------------------------
 constexpr int kQuantThreads = 128;
 
@@ -281,7 +288,9 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize_nv(const void* _
 }
 
 // ------------------------------------------------------------------------------------
-// quantise, BD_FP4_MX: one thread per block of 32 columns, four blocks of scales per 4 lanes
+// quantise, BD_FP4_MX: one thread per block of 32 columns, four blocks of scales per 4 lanes.
+// Bound by HBM and, at a few MB, the ramp of the loads: 512 x 14336 fp32 with x_hat, 62 MB, in
+// 15.7 us (floor 9.6).
 // ------------------------------------------------------------------------------------
 template <int DT, int HAT, bool WIDE>
 __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize_mx(const void* __restrict__ x, int64_t rows, int64_t cols,
@@ -330,7 +339,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize_mx(const void* _
 }
 
 // ------------------------------------------------------------------------------------
-// dequantise: one thread per 32 columns, four such units in flight
+// dequantise: one thread per 32 columns, four such units in flight (one in flight: 38.8 us where
+// this takes 26.7: 14336 x 4096 to bf16, 150 MB, floor 23.0). Bound by HBM's writes.
 // ------------------------------------------------------------------------------------
 template <int FMT, int OUT, bool WIDE>
 __global__ void __launch_bounds__(256) k_fp4_dequantize(const uint8_t* __restrict__ codes,
@@ -417,7 +427,8 @@ __global__ void __launch_bounds__(256) k_fp4_tile_scales(const uint8_t* __restri
 // below 2^-17 of the token's maximum, which is above 3 * 2^8). MX scales hold every power used, and k_t = 0.
 // ------------------------------------------------------------------------------------
 // One CTA per (token, 4096 columns), one thread per 16 columns; in NV every CTA of a token
-// takes the maximum of the whole row (a few loads per thread, all in flight).
+// takes the maximum of the whole row (a few loads per thread, all in flight). Bound by its
+// launch up to a few tokens (about 2 us of a linear call's 6.4); 512 tokens of 4096 take 5 us.
 constexpr int kLimbThreads = 256;
 constexpr int kLimbChunk = kLimbThreads * 16;
 
