@@ -481,7 +481,8 @@ bd_status bd_matmul_fp4(const uint8_t* w_codes, const uint8_t* w_scales, const f
 
 /* bd_linear_fp4 — y[t] = W_hat x[t] with bf16 activations x [tokens][d_in], 16-byte
  * aligned. The tensor cores multiply 4-bit by 4-bit, so each block of x[t] is written as a
- * sum of E2M1 limbs with power-of-two scales: 4 limbs for a BD_BF16 result, 6 for BD_F32.
+ * sum of E2M1 limbs with power-of-two scales: 4 limbs for a BD_BF16 result, 6 for BD_F32 (up to
+ * 4 tokens on small weights are multiplied in fp32 instead, without limbs).
  * With m the block's largest magnitude, values from m/6 up (BD_BF16) or m/384 up (BD_F32) are
  * exact and the others carry at most m * 2^-10 or m * 2^-16; what is smaller than 2^-17 of a
  * token's largest magnitude may be lost in BD_FP4_NV (than 2^-126 in BD_FP4_MX). An infinity

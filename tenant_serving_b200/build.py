@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libbitdelta.so")
 SOURCES = ["bd_abi.cu", "bd_compress.cu", "bd_reconstruct.cu", "bd_apply.cu", "bd_base_tc.cu",
            "bd_prepare.cu", "bd_delta_tc.cu", "bd_delta_lut.cu", "bd_cache.cu",
-           "bd_base_fp8.cu", "bd_fp4.cu", "bd_mm_fp4.cu", "bd_delta_fp4.cu"]
+           "bd_base_fp8.cu", "bd_fp4.cu", "bd_mm_fp4.cu", "bd_gemv_fp4.cu", "bd_delta_fp4.cu"]
 HEADERS = ["bd_internal.cuh", "bd_tc.cuh", "bd_fp4.cuh", "bd_fp4_mma.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -17,7 +17,7 @@ static const char* const kKernelNames[kKindCount] = {
     "quant_fp8",         "x_limbs",      "base_fp8",
     "fp4_quant",         "fp4_dequant",  "fp4_tile_scales",
     "fp4_limbs",         "fp4_mm",       "fp4_seg_limbs",
-    "delta_fp4",
+    "delta_fp4",         "fp4_gemv",
 };
 
 const char* kernel_name(int32_t kind) {

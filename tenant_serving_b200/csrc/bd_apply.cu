@@ -470,12 +470,9 @@ bd_status apply_impl(const void* w_base, int32_t w_dtype, int64_t d_out, int64_t
     if (st != BD_OK) return st;
   } else if (fp4) {
     const int fmt = base - kBaseFp4;
-    uint8_t *xc = ws + L.off_x8, *xs = ws + L.off_x4s;
-    float* xmul = reinterpret_cast<float*>(ws + L.off_xmul);
-    bd_status st = launch_fp4_limbs(L.f4, fmt, x, d_in, batch, xc, xs, xmul, nullptr, s);
-    if (st != BD_OK) return st;
-    st = launch_fp4_mm(L.f4, fmt, Fp4Mat{static_cast<const uint8_t*>(w_base), w_bscales, w_scales},
-                       Fp4Mat{xc, xs, xmul}, d_out, d_in, batch, y_part, BD_F32, status, s);
+    const Fp4Mat w{static_cast<const uint8_t*>(w_base), w_bscales, w_scales};
+    const bd_status st = launch_fp4_linear(L.f4, fmt, w, x, d_out, d_in, batch, ws + L.off_x8, ws + L.off_x4s,
+                                           reinterpret_cast<float*>(ws + L.off_xmul), y_part, BD_F32, nullptr, status, s);
     if (st != BD_OK) return st;
   } else if (tc) {
     bd_status st = launch_base_tc(L.tc, w_base, x, d_out, d_in, batch, y_part, status, s);

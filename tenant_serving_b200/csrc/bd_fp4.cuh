@@ -17,6 +17,7 @@ enum Fp4KernelKind : int32_t {
   K_FP4_MM,                    // tcgen05 block-scaled 4-bit product
   K_FP4_SEG_LIMBS,             // limbs of the delta segments' tokens
   K_DELTA_FP4,                 // the tenants' deltas as a 4-bit product + combine
+  K_FP4_GEMV,                  // product with a few bf16 tokens on the CUDA cores
   kKindCount                   // all kinds
 };
 
@@ -150,7 +151,22 @@ constexpr int kFp4LimbsBf16 = 4, kFp4LimbsF32 = 6;
 Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt, bool y_bf16);
 bd_status launch_fp4_limbs(const Fp4Plan& p, int fmt, const void* x, int64_t d_in, int64_t tokens, uint8_t* xc,
                            uint8_t* xs, float* xmul, uint32_t* reset_status, cudaStream_t s);
+// The few-token kernel is bound by its unpacking, so its time grows with tokens * d_out * d_in;
+// the limbs and tensor-core kernels cost two launches. Measured on the device (us, few-token
+// kernel / the others, BD_FP4_NV): 1024 x 4096 1 token 3.0 / 6.1, 4 tokens 5.3 / 6.2;
+// 4096 x 4096 1 token 6.0 / 7.6, 2 tokens 7.5 / 7.7, 4 tokens 10.7 / 7.7; 4096 x 14336 1 token
+// 15.6 / 13.4; 28672 x 4096 1 token 27.7 / 15.9. The border is 2^25.
+constexpr int64_t kFp4GemvTokens = 4;
+inline bool fp4_use_gemv(int64_t d_out, int64_t d_in, int64_t tokens) {
+  return tokens <= kFp4GemvTokens && tokens * d_out * d_in <= (1 << 25);
+}
+bd_status launch_fp4_gemv(int fmt, const Fp4Mat& w, const void* x, int64_t d_out, int64_t d_in, int64_t tokens,
+                          void* y, int32_t y_dtype, uint32_t* reset_status, cudaStream_t s);
 bd_status launch_fp4_mm(const Fp4Plan& p, int fmt, const Fp4Mat& w, const Fp4Mat& x, int64_t d_out, int64_t d_in,
                         int64_t tokens, void* y, int32_t y_dtype, uint32_t* status, cudaStream_t s);
+// y = x W^T with bf16 x: the few-token kernel, or limbs (xc, xs, xmul: the plan's) and launch_fp4_mm
+bd_status launch_fp4_linear(const Fp4Plan& p, int fmt, const Fp4Mat& w, const void* x, int64_t d_out, int64_t d_in,
+                            int64_t tokens, uint8_t* xc, uint8_t* xs, float* xmul, void* y, int32_t y_dtype,
+                            uint32_t* reset_status, uint32_t* status, cudaStream_t s);
 
 }  // namespace bd

@@ -974,6 +974,16 @@ bd_status launch_fp4_mm(const Fp4Plan& p, int fmt, const Fp4Mat& w, const Fp4Mat
   return BD_OK;
 }
 
+bd_status launch_fp4_linear(const Fp4Plan& p, int fmt, const Fp4Mat& w, const void* x, int64_t d_out, int64_t d_in,
+                            int64_t tokens, uint8_t* xc, uint8_t* xs, float* xmul, void* y, int32_t y_dtype,
+                            uint32_t* reset_status, uint32_t* status, cudaStream_t s) {
+  if (fp4_use_gemv(d_out, d_in, tokens))
+    return launch_fp4_gemv(fmt, w, x, d_out, d_in, tokens, y, y_dtype, reset_status, s);
+  const bd_status r = launch_fp4_limbs(p, fmt, x, d_in, tokens, xc, xs, xmul, reset_status, s);
+  if (r != BD_OK) return r;
+  return launch_fp4_mm(p, fmt, w, Fp4Mat{xc, xs, xmul}, d_out, d_in, tokens, y, y_dtype, status, s);
+}
+
 namespace {
 // arguments of both products; BD_OK and *nothing = true for an empty batch
 bd_status check_mm(const Fp4Mat& w, int32_t fmt, int64_t d_out, int64_t d_in, int64_t tokens, const void* x,
@@ -1059,8 +1069,6 @@ extern "C" bd_status bd_linear_fp4(const uint8_t* w_codes, const uint8_t* w_scal
   uint32_t* status = reinterpret_cast<uint32_t*>(ws);
   float* xmul = reinterpret_cast<float*>(ws + L.off_mul);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bd_status r = launch_fp4_limbs(L.p, fmt, x, d_in, tokens, ws + L.off_c, ws + L.off_s, xmul, status, s);
-  if (r != BD_OK) return r;
-  return launch_fp4_mm(L.p, fmt, w, Fp4Mat{ws + L.off_c, ws + L.off_s, xmul}, d_out, d_in, tokens, y, y_dtype,
-                       status, s);
+  return launch_fp4_linear(L.p, fmt, w, x, d_out, d_in, tokens, ws + L.off_c, ws + L.off_s, xmul, y, y_dtype, status,
+                           status, s);
 }

@@ -207,6 +207,50 @@ def test_linear(bd, fmt, out, d_out, d_in, t):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("d_out,d_in", [(1, 32), (33, 4128), (257, 608), (300, 8224)])
+def test_few_tokens(bd, fmt, out, d_out, d_in):
+    """1 to 4 tokens on small weights: fp32 products, no limbs; 5 tokens for comparison. An
+    infinity or a NaN stays with its token, a NaN block with its row."""
+    import torch
+    rng = np.random.default_rng(d_in)
+    w, wh = _packed(bd, rng, d_out, d_in, fmt)
+    w_hat = O.dequantize_fp4(*wh, fmt)
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    xb = activations(rng, 5, d_in)
+    x = O.decode(xb, "bf16")
+    for t in range(1, 6):
+        y, ws = bd.bd_linear_fp4(*w, dev(xb[:t]), fmt, y_dtype=dt)
+        _check(y, *_limit(w_hat, x[:t], fmt, out, t > 4))
+        assert bd.bd_get_status(ws) == (bd.BD_OK, 0)
+    xn = xb[:4].copy()
+    xn[1, d_in // 2], xn[3, d_in - 1] = 0xFF80, 0x7FC0
+    y, _ = bd.bd_linear_fp4(*w, dev(xn), fmt, y_dtype=dt)
+    clean, _ = bd.bd_linear_fp4(*w, dev(xb[:4]), fmt, y_dtype=dt)
+    assert torch.isnan(y[[1, 3]]).all() and torch.equal(y[[0, 2]], clean[[0, 2]])
+    s = wh[1].copy()
+    s[d_out // 2, -1] = 0x7F if fmt == O.FP4_NV else 0xFF
+    y, _ = bd.bd_linear_fp4(w[0], dev(O.tile_scales(s)), w[2], dev(xb[:4]), fmt, y_dtype=dt)
+    keep = [o for o in range(d_out) if o != d_out // 2]
+    assert torch.isnan(y[:, d_out // 2]).all() and torch.equal(y[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_tokens_at_the_ends_of_fp32(bd, fmt):
+    """A token whose unscaled sums pass fp32's largest number beside a tiny one and a NaN."""
+    import torch
+    rng = np.random.default_rng(3)
+    w, wh = _packed(bd, rng, 65, 4128, fmt)
+    xb = bf16_bits(O.decode(activations(rng, 4, 4128), "bf16") * 2.0 ** np.array([[116], [-100], [0], [0]]))
+    xb[2, 9] = 0x7FC0
+    y, _ = bd.bd_linear_fp4(*w, dev(xb), fmt, y_dtype=torch.float32)
+    keep = [0, 1, 3]
+    x = O.decode(xb, "bf16")[keep]
+    _check(y[keep], *_limit(O.dequantize_fp4(*wh, fmt), x, fmt, "f32", False))
+    assert torch.isnan(y[2]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_wide_rows_and_row_scales_of_a_checkpoint(bd, fmt):
     """One fp32 scale per tensor that is no power of two, in either format, and negative rows."""
     rng = np.random.default_rng(8)
@@ -384,7 +428,12 @@ def test_apply_status_and_limits(bd, fmt):
     clean, _ = bd.bd_apply_multi_fp4(*w, table, dev(ids), dev(xb), fmt, y_dtype=torch.float32)
     assert torch.isnan(y[[0, 3]]).all() and torch.equal(y[[1, 2, 4, 5]], clean[[1, 2, 4, 5]])
     one, _ = bd.bd_apply_multi_fp4(*w, table, dev(ids[:1]), dev(xb[:1]), fmt, y_dtype=torch.float32)
-    assert_apply_close(host(one), host(clean)[:1].astype(np.float64), tol=1e-6, per_token=True)
+    # One token's base product is made in fp32, six tokens' from limbs: the two differ by what
+    # six limbs leave of each value and by the two products' fp32 sums (_limit has both), and the
+    # sum with the delta rounds by 2^-24 of itself in each.
+    _, lim = _limit(O.dequantize_fp4(*wh, fmt), O.decode(xb[:1], "bf16"), fmt, "f32", True)
+    clean = host(clean)[:1].astype(np.float64)
+    _check(one, clean, 2 * lim + 2.0 ** -23 * np.abs(clean))
 
 
 @pytest.mark.parametrize("fmt", FMTS)
