@@ -24,7 +24,8 @@
 // 32 ROW tenants and 256 tokens on 6144 x 4096 takes 95 us, with the lookup and fp16
 // tensor-core kernels 228. An item has 256 rows because a stage's barriers are paid per item
 // row block. Without effect or slower: a deeper ring of limbs, a stage's codes made before the
-// wait for its slot, a second MMA warp, two sets of sum warps, shifts on the multiplier.
+// wait for its slot, a second MMA warp, two sets of sum warps, four banks of half the columns,
+// shifts on the multiplier.
 #include "bd_fp4_mma.cuh"
 
 namespace bd {
