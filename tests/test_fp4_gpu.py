@@ -168,7 +168,8 @@ def test_prepare_scales(bd, fmt, rows, cols):
 # ------------------------------------------------------------------------------ products
 SHAPES = [(1, 32, 1), (128, 64, 16), (130, 1056, 7), (257, 608, 77), (1000, 4096, 33), (64, 14336, 129),
           (520, 800, 300), (300, 256, 700), (2050, 320, 1030),
-          (770, 2112, 300), (130, 2080, 1000)]  # (K split between pairs)
+          (770, 2112, 300), (130, 2080, 1000),  # (K split between pairs)
+          (1001, 512, 600), (33, 96, 300), (259, 2080, 530)]  # (rows of y on odd addresses)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
