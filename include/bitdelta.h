@@ -484,9 +484,10 @@ bd_status bd_matmul_fp4(const uint8_t* w_codes, const uint8_t* w_scales, const f
  * sum of E2M1 limbs with power-of-two scales: 4 limbs for a BD_BF16 result, 6 for BD_F32 (up to
  * 4 tokens on small weights are multiplied in fp32 instead, without limbs).
  * With m the block's largest magnitude, values from m/6 up (BD_BF16) or m/384 up (BD_F32) are
- * exact and the others carry at most m * 2^-10 or m * 2^-16; what is smaller than 2^-17 of a
- * token's largest magnitude may be lost in BD_FP4_NV (than 2^-126 in BD_FP4_MX). An infinity
- * or a NaN in x[t] makes all of y[t] NaN.
+ * exact and the others carry at most m * 2^-10 or m * 2^-16; in BD_FP4_NV also at most 2^-27 or
+ * 2^-33 of the token's largest (in BD_FP4_MX less than 2^-127). Each limb's scale follows what the
+ * limbs before it left, so the error is mostly far smaller: the block's others lose bits only
+ * to what an outlier's own 8 bits need. An infinity or a NaN in x[t] makes all of y[t] NaN.
  *   workspace : bd_linear_fp4_workspace_size() bytes, 16-byte aligned; its status word is reset
  *               by this call. tokens may be 0 (nothing is launched). */
 size_t bd_linear_fp4_workspace_size(int64_t d_out, int64_t d_in, int64_t tokens);

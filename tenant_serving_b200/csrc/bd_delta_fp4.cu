@@ -176,19 +176,15 @@ __global__ void __launch_bounds__(128) k_fp4_seg_limbs(const int32_t* __restrict
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[i])));
-    const uint32_t am = __float_as_uint(m) & 0x7FFFFFFFu;
-    const bool bad = am >= 0x7F800000u;
-    int e = bad ? 0 : (int)(am >> 23) - 127 - 2 + ((am & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-    if (e < -127) e = -127;
+    const bool bad = (__float_as_uint(m) & 0x7FFFFFFFu) >= 0x7F800000u;
     if (bad) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0.f;
     }
 #pragma unroll
     for (int l = 0; l < L; ++l) {
-      const int el = e - (l == 0 ? 0 : 3 * l - 1);
-      const bool live = el >= -127;
-      const float up = live ? pow2f(-el) : 0.f, s = live ? pow2f(el) : 0.f;
+      const int e = max(limb_exponent(__float_as_uint(abs_max<32>(v))), -127);
+      const float up = pow2f(-e), s = pow2f(e);
       uint32_t w[4];
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
@@ -207,7 +203,7 @@ __global__ void __launch_bounds__(128) k_fp4_seg_limbs(const int32_t* __restrict
       const int r = l * gs + j;
       *reinterpret_cast<uint4*>(xc + ((int64_t)seg * kFp4SegRows + r) * (d_in >> 1) + b * 16) =
           make_uint4(w[0], w[1], w[2], w[3]);
-      sb[r * 16] = (uint8_t)(bad ? 0xFFu : (live ? (uint32_t)(el + 127) : 0u));
+      sb[r * 16] = (uint8_t)(bad ? 0xFFu : (uint32_t)(e + 127));
     }
   }
 }

@@ -416,15 +416,23 @@ __global__ void __launch_bounds__(256) k_fp4_tile_scales(const uint8_t* __restri
 }
 
 // ------------------------------------------------------------------------------------
-// activations -> limbs: x_t = 2^k_t * sum_l s_l * e2m1_l per block, s_0 the least power of
-// two with max|block| <= 6 s_0, s_1 = s_0 / 4, and each further one an eighth of the one
-// before: limb 0 leaves a remainder of at most s_0 = 4 s_1 (half a step between 4 and 6),
-// limb l at most s_l / 2 = 4 s_{l+1}. A bf16 value has 8 significant bits, so with L limbs it
-// is exact when its lowest bit is s_{L-1} or more (from s_0 / 2 of its block up with 4
-// limbs, from s_0 / 128 with 6); smaller values end within s_{L-1} / 2 (s_0 / 512, s_0 / 32768).
+// activations -> limbs: x_t = 2^k_t * sum_l s_l * e2m1_l per block, s_l the least power of two
+// with max|what limbs 0 .. l-1 left| <= 6 s_l. Limb 0 leaves at most s_0 (half a step between 4 and
+// 6), which is within 4 of s_0 / 4; a limb that is given at most 4 s_l leaves at most s_l / 2, within
+// 4 of s_l / 8: so s_1 <= s_0 / 4, s_{l+1} <= s_l / 8 from there (a smaller scale has a finer
+// grid wherever it reaches, so it leaves no more), and the smallest limb leaves at most half of
+// s_{L-1} <= s_0 / 2^limb_shift(L-1): s_0 / 512 with 4 limbs, s_0 / 32768 with 6. A bf16 value has 8
+// significant bits, so with L limbs it is exact from s_0 / 2 of its block up with 4 limbs, from
+// s_0 / 128 with 6. Scales that follow what is left, instead of falling by 4, 8, 8, ... whatever
+// is left, cost a maximum per limb and gain most where it counts: behind an outlier that the
+// first limbs hold exactly the others start again from the block's own size (relative error of a
+// product, K = 4096, NV: Gaussian tokens 3e-5 instead of 1.1e-4 with 4 limbs, 2e-8 instead of 2e-7
+// with 6; one value of 4e4 at weights of zero 7e-3 instead of 6e-2, 5e-5 instead of 2e-2).
 // NV scales are E4M3, which holds powers of two from 2^-9 to 2^8 only: k_t puts the token's
-// largest block at s_0 = 2^8, and limbs below 2^-9 are dropped (an error of at most 2^-8,
-// below 2^-17 of the token's maximum, which is above 3 * 2^8). MX scales hold every power used, and k_t = 0.
+// largest block at s_0 <= 2^8, and limb l's scale is stored 2^limb_shift(l) larger than it is (the
+// product's epilogue takes that off again), so that every limb has the whole range. What a block
+// loses to the lowest scale is at most half of 2^-9 / 2^limb_shift(L-1), which is 2^-27 (4 limbs) or
+// 2^-33 (6) of the token's maximum, above 3 * 2^8. MX scales hold every power used, and k_t = 0.
 // ------------------------------------------------------------------------------------
 // One CTA per (token, 4096 columns), one thread per 16 columns; in NV every CTA of a token
 // takes the maximum of the whole row (a few loads per thread, all in flight). Bound by its
@@ -482,21 +490,20 @@ __global__ void __launch_bounds__(kLimbThreads) k_fp4_limbs(const uint16_t* __re
 #pragma unroll
   for (int j = 0; j < 16; ++j) bm = max(bm, abs_bits(v[j]));
   if (FMT == BD_FP4_MX) bm = max(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-  if (!in) return;  // (two threads of an MX block go together)
+  const uint32_t pair = __ballot_sync(0xffffffffu, in);  // (the two threads of an MX block go together)
+  if (!in) return;
   const bool bad = bm >= kInfBits;
   const float down = pow2f(-k);
-  // s_0 = 2^e: least e with max|v| <= 6 * 2^e = 1.5 * 2^(e + 2)
-  const uint32_t am = bad ? 0u : abs_bits(__uint_as_float(bm) * down);
-  int e = (int)(am >> 23) - 127 - 2 + ((am & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-  if (e < kLow) e = kLow;
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = bad ? 0.f : v[j] * down;
   const int64_t b = c / kBlock;
 #pragma unroll
   for (int l = 0; l < L; ++l) {
-    const int el = e - (l == 0 ? 0 : 3 * l - 1);
-    const bool live = el >= kLow;
-    const float up = live ? pow2f(-el) : 0.f, s = live ? pow2f(el) : 0.f;
+    const int shift = FMT == BD_FP4_NV ? limb_shift(l) : 0;
+    float m = abs_max<16>(v);
+    if (FMT == BD_FP4_MX) m = fmaxf(m, __shfl_xor_sync(pair, m, 1));
+    const int e = max(limb_exponent(__float_as_uint(m)), kLow - shift);
+    const float up = pow2f(-e), s = pow2f(e);
     float q[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) q[j] = v[j] * up;
@@ -511,10 +518,10 @@ __global__ void __launch_bounds__(kLimbThreads) k_fp4_limbs(const uint16_t* __re
     const int64_t row = row0 + 8 * l;
     *reinterpret_cast<uint2*>(xc + row * (d_in >> 1) + (c >> 1)) = p;
     uint32_t code;
-    if (FMT == BD_FP4_NV)  // E4M3: 2^el is a normal code from 2^-6 on, then 4, 2, 1
-      code = bad ? 0x7Fu : (!live ? 0u : (el >= -6 ? (uint32_t)(el + 7) << 3 : 1u << (el + 9)));
+    if (FMT == BD_FP4_NV)  // E4M3: 2^es is a normal code from 2^-6 on, then 4, 2, 1
+      code = bad ? 0x7Fu : (e + shift >= -6 ? (uint32_t)(e + shift + 7) << 3 : 1u << (e + shift + 9));
     else
-      code = bad ? 0xFFu : (!live ? 0u : (uint32_t)(el + 127));
+      code = bad ? 0xFFu : (uint32_t)(e + 127);
     if (FMT == BD_FP4_NV || (threadIdx.x & 1) == 0)
       xs[fp4_scale_row(row, tiles_k) + (b >> 2) * kFp4TileBytes + (b & 3)] = (uint8_t)code;
   }

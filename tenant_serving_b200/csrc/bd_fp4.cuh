@@ -110,6 +110,22 @@ __device__ __forceinline__ float fp4_scale_value(uint32_t code) {
   return code == 0xFFu ? __uint_as_float(0x7FFFFFFFu) : pow2f((int)code - 127);
 }
 
+// Limbs of a block of activations (bd_fp4.cu, bd_delta_fp4.cu): limb l has scale 2^e with the
+// least e for which 6 * 2^e holds the largest magnitude of what the limbs before it left. `bits`
+// are that magnitude's (6 = 1.5 * 2^2); what fp32 holds as a subnormal gives less than -127.
+__device__ __forceinline__ int limb_exponent(uint32_t bits) {
+  return (int)(bits >> 23) - 127 - 2 + ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+}
+// largest of N magnitudes, as a tree (the limbs' maxima are on their kernels' longest chain)
+template <int N>
+__device__ __forceinline__ float abs_max(const float* v) {
+  if (N == 2) return fmaxf(fabsf(v[0]), fabsf(v[1]));
+  return fmaxf(abs_max<(N > 2 ? N / 2 : 2)>(v), abs_max<(N > 2 ? N / 2 : 2)>(v + N / 2));
+}
+// limb l > 0 is at least 2^limb_shift(l) smaller than limb 0: the limb before leaves at most half a
+// step, which is s_0 = 6 (s_0 / 4) / 1.5 after limb 0 and 4 s_{l+1} = s_l / 2 after a further one
+__host__ __device__ constexpr int limb_shift(int l) { return l == 0 ? 0 : 3 * l - 1; }
+
 // Launch plan of a 4-bit product D[W rows][X rows]. X rows are tokens, or `limbs` rows per
 // token: N tile j holds h tokens from row j * n_stride, limb l of its token t in row
 // (t / 8) * 8 * limbs + 8 * l + t % 8.

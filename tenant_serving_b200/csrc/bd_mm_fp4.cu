@@ -74,8 +74,9 @@ struct Group {
   static constexpr int kCols = L == 1 ? 32 : 8 * L;
   static constexpr int kTok = kCols / L;
 };
-// sums of a group's tokens, the smallest limb first
-template <int L>
+// Sums of a group's tokens, the smallest limb first. In BD_FP4_NV limb l's columns are
+// 2^limb_shift(l) too large: each step takes what lies between two limbs off.
+template <int FMT, int L>
 __device__ __forceinline__ void load_group(uint32_t taddr, float* v) {
   uint32_t r[Group<L>::kCols];
   tmem_load<32>(taddr, r);
@@ -85,7 +86,10 @@ __device__ __forceinline__ void load_group(uint32_t taddr, float* v) {
   for (int j = 0; j < Group<L>::kTok; ++j) {
     float a = __uint_as_float(r[8 * (L - 1) + j]);
 #pragma unroll
-    for (int l = L - 2; l >= 0; --l) a += __uint_as_float(r[8 * l + j]);
+    for (int l = L - 2; l >= 0; --l) {
+      const float down = FMT == BD_FP4_NV ? 1.f / (float)(1 << (limb_shift(l + 1) - limb_shift(l))) : 1.f;
+      a = fmaf(a, down, __uint_as_float(r[8 * l + j]));
+    }
     v[j] = a;
   }
 }
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
     const float rs = in && p.w_row ? p.w_row[row] : 1.f;
     for (int c0 = set * kTok; c0 < n_tok; c0 += 2 * kTok) {
       float v[kTok];
-      load_group<L>(lane_addr + (uint32_t)(c0 * L), v);
+      load_group<FMT, L>(lane_addr + (uint32_t)(c0 * L), v);
 #pragma unroll
       for (int j = 0; j < kTok; ++j)
         if (in && c0 + j < n_tok) store_y(p, t0 + c0 + j, row, v[j] * rs * xr[c0 + j]);
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kMmThreads) k_fp4_mm_rows(const __grid_constan
   const uint32_t mine = smem_u32(gather + (size_t)rank * share * 128 + r0);
   for (int c0 = set * kTok; c0 < n_tok; c0 += 2 * kTok) {
     float v[kTok];
-    load_group<L>(lane_addr + (uint32_t)(c0 * L), v);
+    load_group<FMT, L>(lane_addr + (uint32_t)(c0 * L), v);
 #pragma unroll
     for (int j = 0; j < kTok; ++j)
       if (c0 + j < n_tok) {
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int q = set; q < kGroups; q += 2) {
         const int g = group_of(q);
         float v[kTok];
-        load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
+        load_group<FMT, L>(at + (uint32_t)(g * Group<L>::kCols), v);
         if (q == set) {
           tc_fence_before();
           __syncwarp();
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp >= 4)
       for (int g = far0 + set; g < far1; g += 2) {
         float v[kTok];
-        load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
+        load_group<FMT, L>(at + (uint32_t)(g * Group<L>::kCols), v);
         const uint32_t to = map_cluster(smem_u32(sums + (g - far0) * kTok * 128 + r0), (uint32_t)(rank ^ 2));
 #pragma unroll
         for (int c = 0; c < kTok; ++c) st_cluster_f32(to + c * 512, v[c]);
@@ -747,7 +751,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int g = own0 + set; g < own1; g += 2) {
         const float xs = token_scale(t0, g);
         float v[kTok];
-        load_group<L>(at + (uint32_t)(g * Group<L>::kCols), v);
+        load_group<FMT, L>(at + (uint32_t)(g * Group<L>::kCols), v);
 #pragma unroll
         for (int c = 0; c < kTok; ++c) v[c] += sums[((g - own0) * kTok + c) * 128 + r0];
         emit(row0, t0, g, rs, xs, v);

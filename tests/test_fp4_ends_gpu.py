@@ -1,0 +1,98 @@
+"""The 4-bit operators where values leave the middle of their ranges."""
+
+import numpy as np
+import pytest
+
+import oracle as O
+from helpers import dev, host
+from test_fp4_gpu import _check, _packed
+from workloads import activations, bf16_bits
+
+pytestmark = pytest.mark.gpu
+FMTS = [O.FP4_NV, O.FP4_MX]
+
+
+@pytest.fixture(scope="module")
+def bd():
+    from tenant_serving_b200 import build
+    build.build()
+    import tenant_serving_b200 as m
+    return m
+
+
+def _dtype(out):
+    import torch
+    return torch.float32 if out == "f32" else torch.bfloat16
+
+
+def _bound(y, w_hat, x, e, out):
+    """Allowed error of y = x w_hat^T whose activations are off by e: fp32 sums over K = 64 steps,
+    their joins and the scales (see test_fp4_gpu), and a bf16 result's own rounding."""
+    lim = (w_hat.shape[1] / 64 + 16) * 2.0 ** -23 * (np.abs(x) @ np.abs(w_hat).T) + e @ np.abs(w_hat).T
+    return lim + (2.0 ** -8 * (np.abs(y) + lim) if out == "bf16" else 0)
+
+
+def _no_weight_at(wh, cols):
+    """The matrix with code 0 or 8 in some columns: (codes, scales, row)."""
+    codes = wh[0].copy()
+    for c in cols:
+        codes[:, c // 2] &= 0x8F if c % 2 else 0xF8
+    return codes, wh[1], wh[2]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [5, 70])
+def test_linear_keeps_what_stands_beside_a_massive_value(bd, fmt, out, t):
+    """One value 4 10^4 times the others, alone in its block and at weights of zero: the result
+    is made of the small values of the token's other blocks, which keep their own precision. L limbs
+    leave an element at most 2^-(3 L - 2) of its block's largest, and in BD_FP4_NV no less than
+    2^-27 (4 limbs) or 2^-33 (6) of the token's largest."""
+    rng = np.random.default_rng(t)
+    d_out, d_in, at = 130, 1056, 96
+    _, wh = _packed(bd, rng, d_out, d_in, fmt)
+    wh = _no_weight_at(wh, [at])
+    w_hat = O.dequantize_fp4(*wh, fmt)
+    assert (w_hat[:, at] == 0).all()
+    x = O.decode(activations(rng, t, d_in), "bf16")
+    x[:, at: at + O.fp4_block(fmt)] = 0
+    x[:, at] = 4e4 * np.abs(x).mean() * rng.uniform(0.5, 1, size=t)
+    xb = bf16_bits(x)
+    x = O.decode(xb, "bf16")
+    b = O.fp4_block(fmt)
+    e = np.abs(x).reshape(t, -1, b).max(2).repeat(b, 1) * (2.0 ** -16 if out == "f32" else 2.0 ** -10)
+    if fmt == O.FP4_NV:
+        e = e + np.abs(x).max(1, keepdims=True) * (2.0 ** -33 if out == "f32" else 2.0 ** -27)
+    x[:, at] = e[:, at] = 0   # (what has no weight takes part in nothing)
+    y, ws = bd.bd_linear_fp4(dev(wh[0]), dev(O.tile_scales(wh[1])), None if wh[2] is None else dev(wh[2]), dev(xb), fmt,
+                             y_dtype=_dtype(out))
+    assert bd.bd_get_status(ws) == (bd.BD_OK, 0)
+    ref = x @ w_hat.T
+    _check(y, ref, _bound(ref, w_hat, x, e, out))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [5, 70])
+def test_linear_keeps_what_stands_beside_an_outlier_of_its_block(bd, fmt, out, t):
+    """A power of two, 2^13 times the rest, in every block: one limb holds it exactly, and the
+    block's others, n the largest of them, have the remaining L - 1: n 2^-(3 (L - 1) - 2)."""
+    rng = np.random.default_rng(t)
+    d_out, d_in = 130, 1056
+    b = O.fp4_block(fmt)
+    at = np.arange(0, d_in, b) + rng.integers(0, b, size=d_in // b)
+    _, wh = _packed(bd, rng, d_out, d_in, fmt)
+    wh = _no_weight_at(wh, at)
+    w_hat = O.dequantize_fp4(*wh, fmt)
+    x = rng.uniform(0.25, 1, size=(t, d_in)) * rng.choice([-1, 1], size=(t, d_in))
+    x[:, at] = 2.0 ** 13
+    xb = bf16_bits(x)
+    x = O.decode(xb, "bf16")
+    x[:, at] = 0
+    e = np.abs(x).reshape(t, -1, b).max(2).repeat(b, 1) * (2.0 ** -13 if out == "f32" else 2.0 ** -7)
+    if fmt == O.FP4_NV:
+        e += 2.0 ** 13 * (2.0 ** -33 if out == "f32" else 2.0 ** -27)
+    y, _ = bd.bd_linear_fp4(dev(wh[0]), dev(O.tile_scales(wh[1])), None if wh[2] is None else dev(wh[2]), dev(xb), fmt,
+                            y_dtype=_dtype(out))
+    ref = x @ w_hat.T
+    _check(y, ref, _bound(ref, w_hat, x, e, out))
