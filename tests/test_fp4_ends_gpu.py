@@ -96,3 +96,67 @@ def test_linear_keeps_what_stands_beside_an_outlier_of_its_block(bd, fmt, out, t
                             y_dtype=_dtype(out))
     ref = x @ w_hat.T
     _check(y, ref, _bound(ref, w_hat, x, e, out))
+
+
+# rows kernel alone and with K split over a cluster, pair kernel alone and with K split
+ENDS = [(130, 256, 7), (64, 4096, 20), (300, 512, 300), (256, 2304, 300)]
+
+
+def _scaled(rng, n, exponent):
+    return (rng.uniform(1, 2, size=n) * 2.0 ** exponent * rng.choice([-1, 1], size=n)).astype(np.float32)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("ew,ex", [(115, -110), (-110, 115), (60, 30), (-50, -30)])
+@pytest.mark.parametrize("d_out,d_in,t", ENDS)
+def test_row_scales_of_opposite_ends(bd, fmt, out, ew, ex, d_out, d_in, t):
+    """Huge weights meet tiny tokens and the reverse: no product on the way to a result of
+    ordinary size leaves fp32's range."""
+    rng = np.random.default_rng(d_in + t)
+    w, wh = _packed(bd, rng, d_out, d_in, fmt)
+    x, xh = _packed(bd, rng, t, d_in, fmt)
+    wr, xr = _scaled(rng, d_out, ew), _scaled(rng, t, ex)
+    y, ws = bd.bd_matmul_fp4(w[0], w[1], dev(wr), x[0], x[1], dev(xr), fmt, y_dtype=_dtype(out))
+    assert bd.bd_get_status(ws) == (bd.BD_OK, 0)
+    w_hat, x_hat = O.dequantize_fp4(wh[0], wh[1], wr, fmt), O.dequantize_fp4(xh[0], xh[1], xr, fmt)
+    ref = x_hat @ w_hat.T
+    assert np.abs(ref).max() < 2.0 ** 127
+    _check(y, ref, _bound(ref, w_hat, x_hat, 0 * x_hat, out))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("ew,ex", [(-30, 60), (60, -30)])
+@pytest.mark.parametrize("d_out,d_in,t", ENDS)
+def test_row_scales_of_tiny_blocks(bd, out, ew, ex, d_out, d_in, t):
+    """Block scales of 2^-60 on both sides: sums near 2^-115 that one of the scales would take
+    into the subnormals before the other brings them back."""
+    rng = np.random.default_rng(d_in + t)
+    fmt = O.FP4_MX
+    c = [rng.integers(0, 256, size=(n, d_in // 2), dtype=np.uint8) for n in (d_out, t)]
+    s = [rng.integers(64, 70, size=(n, d_in // 32), dtype=np.uint8) for n in (d_out, t)]
+    wr, xr = _scaled(rng, d_out, ew), _scaled(rng, t, ex)
+    y, _ = bd.bd_matmul_fp4(dev(c[0]), dev(O.tile_scales(s[0])), dev(wr), dev(c[1]), dev(O.tile_scales(s[1])), dev(xr), fmt,
+                            y_dtype=_dtype(out))
+    w_hat, x_hat = O.dequantize_fp4(c[0], s[0], wr, fmt), O.dequantize_fp4(c[1], s[1], xr, fmt)
+    ref = x_hat @ w_hat.T
+    _check(y, ref, _bound(ref, w_hat, x_hat, 0 * x_hat, out))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("t", [4, 5, 70])
+def test_linear_of_huge_weights_and_tiny_tokens(bd, out, t):
+    """Weights of 1e35 as bd_quantize_fp4 holds them, tokens of 1e-30: finite, whether the
+    tokens are few enough for the fp32 kernel or go through limbs."""
+    rng = np.random.default_rng(t)
+    w = (rng.normal(size=(100, 1056)) * 1e35).astype(np.float32)
+    q = O.quantize_fp4(w, "f32", O.FP4_NV)
+    codes, scales, row, _ = bd.bd_quantize_fp4(dev(w), O.FP4_NV)
+    xb = bf16_bits(O.decode(activations(rng, t, 1056), "bf16") * 1e-30)
+    x = O.decode(xb, "bf16")
+    y, _ = bd.bd_linear_fp4(codes, scales, row, dev(xb), O.FP4_NV, y_dtype=_dtype(out))
+    w_hat = O.dequantize_fp4(*q, O.FP4_NV)
+    ref = x @ w_hat.T
+    e = np.abs(x).reshape(t, -1, 16).max(2).repeat(16, 1) * (2.0 ** -16 if out == "f32" else 2.0 ** -10)
+    e = e + np.abs(x).max(1, keepdims=True) * (2.0 ** -33 if out == "f32" else 2.0 ** -27)
+    _check(y, ref, _bound(ref, w_hat, x, e, out))
