@@ -143,7 +143,7 @@ __device__ __forceinline__ bool finite(float m) { return abs_bits(m) < kInfBits;
 // border b of E2M1, v = b s is an fp32 number, so q = b exactly there, and a v beside it
 // differs by a whole unit in its last place, more than q's rounding can undo.
 template <int HAT, bool WIDE>
-__device__ __forceinline__ uint2 encode16(const float* v, bool bad, float down, float s, float y, float r, void* hat_row,
+__device__ __forceinline__ uint2 encode16(const float* v, bool none, float down, float s, float y, float r, void* hat_row,
                                           int64_t c) {
   float q[16];
 #pragma unroll
@@ -151,7 +151,7 @@ __device__ __forceinline__ uint2 encode16(const float* v, bool bad, float down, 
     const float a = v[j] * down, q0 = a * y;
     q[j] = fmaf(-fmaf(q0, s, -a), y, q0);  // (this way round a zero keeps its sign)
   }
-  if (bad) {
+  if (none) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) q[j] = 0.f;
   }
@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp4_quantize_nv(const void* _
     if (in) {
       float v[16];
       widen<DT>(w, v);
-      const uint2 p = encode16<HAT, WIDE>(v, bad, s > 0.f ? down : 0.f, s, s > 0.f ? 1.0f / s : 0.f, r, hr, c);
+      const bool none = !(s > 0.f);  // a scale of 0 or NaN: the codes are 0, without the values' signs
+      const uint2 p = encode16<HAT, WIDE>(v, none, down, s, none ? 0.f : 1.0f / s, r, hr, c);
       *reinterpret_cast<uint2*>(codes + row * (cols >> 1) + (c >> 1)) = p;
     }
   };

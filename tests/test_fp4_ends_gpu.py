@@ -160,3 +160,28 @@ def test_linear_of_huge_weights_and_tiny_tokens(bd, out, t):
     e = np.abs(x).reshape(t, -1, 16).max(2).repeat(16, 1) * (2.0 ** -16 if out == "f32" else 2.0 ** -10)
     e = e + np.abs(x).max(1, keepdims=True) * (2.0 ** -33 if out == "f32" else 2.0 ** -27)
     _check(y, ref, _bound(ref, w_hat, x, e, out))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("hat", [None, "f32", "bf16"])
+def test_blocks_whose_scale_is_zero(bd, fmt, dtype, hat):
+    """Negative values, and zeros with a sign, in blocks far below the row's largest: where the
+    block scale rounds to zero the codes are 0."""
+    x = np.zeros((4, 96), dtype=np.float32)
+    x[0, 0], x[0, 16:32], x[0, 48:64] = 1000, -1e-6, -1e-7
+    x[1, 5], x[1, 32:48], x[1, 64:] = -2000, -0.0, -1e-6
+    x[2] = -0.0
+    x[3, :48], x[3, 48:] = 3, np.where(np.arange(48) % 2, -1e-7, 1e-7)
+    if dtype == "bf16":
+        x = bf16_bits(x)
+    elif dtype == "f16":
+        x = x.astype(np.float16)
+    codes, scales, row, h = bd.bd_quantize_fp4(dev(x, dtype), fmt, hat_dtype=None if hat is None else _dtype(hat))
+    c, s, r = O.quantize_fp4(x, dtype, fmt)
+    assert np.array_equal(host(scales), O.tile_scales(s)) and np.array_equal(host(codes), c)
+    if hat is not None:
+        got = host(h)
+        got = O.decode(got, "bf16") if hat == "bf16" else got.astype(np.float64)
+        ref = O.dequantize_fp4(c, s, r, fmt)
+        assert np.array_equal(got, ref) and np.array_equal(np.signbit(got), np.signbit(ref))
