@@ -16,18 +16,16 @@ typedef CUresult (*TensorMapEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint3
                                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                       CUtensorMapFloatOOBfill);
 inline TensorMapEncodeFn tensor_map_encoder() {
-  static TensorMapEncodeFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+  // (a local static: a second thread's first call waits until the look-up is over)
+  static const TensorMapEncodeFn fn = []() -> TensorMapEncodeFn {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<TensorMapEncodeFn>(p);
-    else
-      (void)cudaGetLastError();
-  }
+      return reinterpret_cast<TensorMapEncodeFn>(p);
+    (void)cudaGetLastError();
+    return nullptr;
+  }();
   return fn;
 }
 
