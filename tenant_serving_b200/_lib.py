@@ -434,12 +434,14 @@ _FP4 = {}  # torch, its dtypes' codes and the entry points, filled on first use
 
 
 def _fp4_env():
+    # (other threads take _FP4 for complete as soon as it holds anything: it is filled at once)
     torch = _torch()
-    _FP4["torch"], _FP4["u8"], _FP4["f32"], _FP4["bf16"] = torch, torch.uint8, torch.float32, torch.bfloat16
-    _FP4["code"] = {torch.float32: BD_F32, torch.bfloat16: BD_BF16, torch.float16: BD_F16}
-    _FP4["device"] = torch.cuda.current_device
-    _FP4["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _FP4.update({
+        "torch": torch, "u8": torch.uint8, "f32": torch.float32, "bf16": torch.bfloat16,
+        "code": {torch.float32: BD_F32, torch.bfloat16: BD_BF16, torch.float16: BD_F16},
+        "device": torch.cuda.current_device,
+        "stream": getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+        (lambda dev: torch.cuda.current_stream(dev).cuda_stream)})
     return _FP4
 
 

@@ -4,10 +4,12 @@ for the second thread too. No GPU: the look-ups are slowed down by stand-ins."""
 import os
 import shutil
 import subprocess
+import threading
 
 import pytest
 
-from tenant_serving_b200 import build
+import tenant_serving_b200 as bd
+from tenant_serving_b200 import _lib, build
 
 ENCODER = r"""
 #include <cuda.h>
@@ -58,3 +60,37 @@ def test_tensor_map_encoder(tmp_path):
                    capture_output=True, text=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert (r.returncode, r.stdout.strip()) == (0, "8")
+
+
+class _SlowTorch:
+    """torch whose attributes take a while: a second thread gets in between any two of them."""
+
+    def __init__(self, torch, step):
+        self._torch, self._step = torch, step
+
+    def __getattr__(self, name):
+        self._step()
+        return getattr(self._torch, name)
+
+
+def test_what_the_4_bit_calls_keep(monkeypatch):
+    import torch
+    monkeypatch.setattr(_lib, "_FP4", {})
+    seen, failed = [], []
+
+    def other():
+        try:
+            seen.append(_lib._fp4_code(torch.zeros(1, dtype=torch.bfloat16)))
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    def step():
+        if _lib._FP4:  # the first thread is not done, the others already take it for complete
+            t = threading.Thread(target=other)
+            t.start()
+            t.join()
+
+    monkeypatch.setattr(_lib, "_torch", lambda: _SlowTorch(torch, step))
+    assert _lib._fp4_code(torch.zeros(1, dtype=torch.float32)) == bd.BD_F32
+    other()
+    assert not failed and seen and set(seen) == {bd.BD_BF16}
