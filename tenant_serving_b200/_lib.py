@@ -487,6 +487,15 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _made_on(stream, make, *args):
+    """What a call allocates belongs to the stream that it launches on: fills come before its
+    kernels, and memory that is dropped goes to that stream's next allocation, not to another's."""
+    if stream is None:
+        return make(*args)
+    with (_FP4 or _fp4_env())["torch"].cuda.stream(stream):
+        return make(*args)
+
+
 def bd_fp4_scales_bytes(rows, cols, fmt) -> int:
     return int(lib().bd_fp4_scales_bytes(int(rows), int(cols), int(fmt)))
 
@@ -539,10 +548,13 @@ def _fp4_shape(codes, scales, row_scales, fmt, where):
     return rows, cols
 
 
-def _fp4_out(y, rows, cols, dtype, like, where):
+def _fp4_empty(shape, dtype, device):
+    return (_FP4 or _fp4_env())["torch"].empty(shape, dtype=dtype, device=device)
+
+
+def _fp4_out(y, rows, cols, dtype, like, where, stream):
     if y is None:
-        torch = _torch()
-        return torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=like.device)
+        return _made_on(stream, _fp4_empty, (rows, cols), dtype or (_FP4 or _fp4_env())["bf16"], like.device)
     if y.shape != (rows, cols) or not y.is_contiguous():
         raise BitDeltaError(BD_ERR_SHAPE, where)
     return y
@@ -555,7 +567,7 @@ def bd_prepare_fp4_scales(scales, fmt, rows, cols, out=None, stream=None):
     where = "bd_prepare_fp4_scales"
     n = bd_fp4_scales_bytes(rows, cols, fmt)
     if out is None and n and scales.is_cuda:
-        out = torch.empty(fp4_scales_shape(rows, cols, fmt), dtype=torch.uint8, device=scales.device)
+        out = _made_on(stream, _fp4_empty, fp4_scales_shape(rows, cols, fmt), torch.uint8, scales.device)
     dev = _on_device((scales, out))
     if n == 0 or scales.element_size() != 1 or not scales.is_contiguous() or not out.is_contiguous() or \
             scales.numel() != rows * (cols // _FP4_BLOCK[fmt]) or out.numel() * out.element_size() != n:
@@ -574,13 +586,13 @@ def bd_quantize_fp4(x, fmt, codes=None, scales=None, row_scales=None, hat=None, 
     if cols > 1 and x.stride(1) != 1:
         raise BitDeltaError(BD_ERR_SHAPE, where)
     if codes is None or scales is None or (row_scales is None and fmt == BD_FP4_NV):
-        c, s, r = fp4_buffers(rows, cols, fmt, x.device)
+        c, s, r = _made_on(stream, fp4_buffers, rows, cols, fmt, x.device)
         codes, scales, row_scales = (codes if codes is not None else c), (scales if scales is not None else s), \
             (row_scales if row_scales is not None else r)
     if _fp4_shape(codes, scales, row_scales, fmt, where) != (rows, cols):
         raise BitDeltaError(BD_ERR_SHAPE, where)
     if hat is not None or hat_dtype is not None:
-        hat = _fp4_out(hat, rows, cols, hat_dtype, x, where)
+        hat = _fp4_out(hat, rows, cols, hat_dtype, x, where, stream)
     _fp4_call(where, dev, (_p(x), _fp4_code(x), rows, cols, x.stride(0) if rows > 1 else cols, fmt, _p(codes),
                            _p(scales), _p(row_scales), _p(hat), _fp4_code(hat) if hat is not None else BD_F32), stream)
     return codes, scales, row_scales, hat
@@ -591,7 +603,7 @@ def bd_dequantize_fp4(codes, scales, row_scales, fmt, out=None, out_dtype=None, 
     where = "bd_dequantize_fp4"
     dev = _on_device((codes, scales, row_scales, out))
     rows, cols = _fp4_shape(codes, scales, row_scales, fmt, where)
-    out = _fp4_out(out, rows, cols, out_dtype, codes, where)
+    out = _fp4_out(out, rows, cols, out_dtype, codes, where, stream)
     _fp4_call(where, dev, (_p(codes), _p(scales), _p(row_scales), fmt, rows, cols, _p(out), _fp4_code(out)), stream)
     return out
 
@@ -610,9 +622,9 @@ def bd_matmul_fp4(w_codes, w_scales, w_row, x_codes, x_scales, x_row, fmt, y=Non
     tokens = x_codes.size(0)
     if tokens and _fp4_shape(x_codes, x_scales, x_row, fmt, where) != (tokens, d_in):
         raise BitDeltaError(BD_ERR_SHAPE, where)
-    y = _fp4_out(y, tokens, d_out, y_dtype, w_codes, where)
+    y = _fp4_out(y, tokens, d_out, y_dtype, w_codes, where, stream)
     if workspace is None:
-        workspace = fp4_workspace(bd_matmul_fp4_workspace_size(d_out, d_in, tokens), w_codes.device)
+        workspace = _made_on(stream, fp4_workspace, bd_matmul_fp4_workspace_size(d_out, d_in, tokens), w_codes.device)
     _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), _p(x_codes), _p(x_scales), _p(x_row), fmt, d_out,
                            d_in, tokens, _p(y), _fp4_code(y), _p(workspace), workspace.nbytes), stream)
     return y, workspace
@@ -637,10 +649,10 @@ def bd_linear_fp4(w_codes, w_scales, w_row, x, fmt, y=None, y_dtype=None, worksp
     dev = _on_device((w_codes, w_scales, w_row, x, y, workspace))
     d_out, d_in = _fp4_shape(w_codes, w_scales, w_row, fmt, where)
     tokens = _bf16_rows(x, d_in, where)
-    y = _fp4_out(y, tokens, d_out, y_dtype, x, where)
+    y = _fp4_out(y, tokens, d_out, y_dtype, x, where, stream)
     if workspace is None:
-        torch = _torch()
-        workspace = torch.empty(bd_linear_fp4_workspace_size(d_out, d_in, tokens), dtype=torch.uint8, device=x.device)
+        workspace = _made_on(stream, _fp4_empty, bd_linear_fp4_workspace_size(d_out, d_in, tokens),
+                             (_FP4 or _fp4_env())["u8"], x.device)
     _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), fmt, d_out, d_in, _p(x), tokens, _p(y),
                            _fp4_code(y), _p(workspace), workspace.nbytes), stream)
     return y, workspace
@@ -662,10 +674,10 @@ def bd_apply_multi_fp4(w_codes, w_scales, w_row, table, tenant_ids, x, fmt, y=No
     batch = _bf16_rows(x, d_in, where)
     if tenant_ids.dtype is not torch.int32 or tenant_ids.numel() != batch or not tenant_ids.is_contiguous():
         raise BitDeltaError(BD_ERR_SHAPE, where)
-    y = _fp4_out(y, batch, d_out, y_dtype, x, where)
+    y = _fp4_out(y, batch, d_out, y_dtype, x, where, stream)
     if workspace is None:
-        workspace = torch.empty(max(bd_apply_fp4_workspace_size(d_out, d_in, batch, table.n), 16),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _made_on(stream, _fp4_empty, max(bd_apply_fp4_workspace_size(d_out, d_in, batch, table.n), 16),
+                             torch.uint8, x.device)
     _fp4_call(where, dev, (_p(w_codes), _p(w_scales), _p(w_row), fmt, d_out, d_in, tab, table.n, table.scale_dtype,
                            _p(tenant_ids), _p(x), batch, _p(y), _fp4_code(y), _p(workspace), workspace.nbytes),
               stream)
