@@ -233,6 +233,15 @@ def _stream(stream):
     return c_void_p(s.cuda_stream)
 
 
+def _made_on(stream, make, *args, **kw):
+    """What a call allocates belongs to the stream that it launches on: fills come before its
+    kernels, and memory that is dropped goes to that stream's next allocation, not to another's."""
+    if stream is None:
+        return make(*args, **kw)
+    with _torch().cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _require_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -269,15 +278,15 @@ def bd_compress(w_base, w_fine, cfg: bd_compress_cfg, signs=None, scales=None, s
     d_out, d_in = w_base.shape
     dev = w_base.device
     if signs is None:
-        signs = torch.empty((d_out, d_in // 32), dtype=torch.int32, device=dev)
+        signs = _made_on(stream, torch.empty, (d_out, d_in // 32), dtype=torch.int32, device=dev)
     if scales is None:
-        scales = torch.empty(scales_shape(cfg.mode, d_out, d_in, cfg.group_size),
-                             dtype=torch.float32, device=dev)
+        scales = _made_on(stream, torch.empty, scales_shape(cfg.mode, d_out, d_in, cfg.group_size),
+                          dtype=torch.float32, device=dev)
     if stats is None and cfg.clip:
-        stats = torch.zeros(4, dtype=torch.float64, device=dev)
+        stats = _made_on(stream, torch.zeros, 4, dtype=torch.float64, device=dev)
     ws = bd_compress_workspace_size(d_out, d_in, cfg)
     if workspace is None:
-        workspace = torch.empty(max(ws, 16), dtype=torch.uint8, device=dev)
+        workspace = _made_on(stream, torch.empty, max(ws, 16), dtype=torch.uint8, device=dev)
     rc = lib().bd_compress(_ptr(w_base), _ptr(w_fine), dtype_code(w_base), d_out, d_in,
                            ctypes.byref(cfg), _ptr(signs), _ptr(scales), _ptr(stats),
                            _ptr(workspace), workspace.numel(), _stream(stream))
@@ -294,12 +303,12 @@ def bd_compress_noalloc(w_base, w_fine, cfg: bd_compress_cfg, signs=None, scales
     d_out, d_in = w_base.shape
     dev = w_base.device
     if signs is None:
-        signs = torch.empty((d_out, d_in // 32), dtype=torch.int32, device=dev)
+        signs = _made_on(stream, torch.empty, (d_out, d_in // 32), dtype=torch.int32, device=dev)
     if scales is None:
-        scales = torch.empty(scales_shape(cfg.mode, d_out, d_in, cfg.group_size),
-                             dtype=torch.float32, device=dev)
+        scales = _made_on(stream, torch.empty, scales_shape(cfg.mode, d_out, d_in, cfg.group_size),
+                          dtype=torch.float32, device=dev)
     if stats is None and cfg.clip:
-        stats = torch.zeros(4, dtype=torch.float64, device=dev)
+        stats = _made_on(stream, torch.zeros, 4, dtype=torch.float64, device=dev)
     rc = lib().bd_compress_noalloc(_ptr(w_base), _ptr(w_fine), dtype_code(w_base), d_out, d_in,
                                    ctypes.byref(cfg), _ptr(signs), _ptr(scales), _ptr(stats),
                                    _stream(stream))
@@ -312,7 +321,7 @@ def bd_reconstruct(signs, scales, mode, group_size, d_out, d_in, w_base=None, ou
     torch = _torch()
     _require_cuda(signs, scales, w_base)
     if out is None:
-        out = torch.empty((d_out, d_in), dtype=out_dtype or torch.float32, device=signs.device)
+        out = _made_on(stream, torch.empty, (d_out, d_in), dtype=out_dtype or torch.float32, device=signs.device)
     rc = lib().bd_reconstruct(_ptr(signs), _ptr(scales), dtype_code(scales), int(mode),
                               int(group_size), int(d_out), int(d_in), _ptr(w_base),
                               dtype_code(w_base) if w_base is not None else BD_F32, _ptr(out),
@@ -331,8 +340,8 @@ def bd_prepare_tenant(signs, scales, mode, group_size, d_out, d_in, stream=None)
     ns = int(lib().bd_prepared_scales_bytes(int(d_out), int(d_in), int(mode), int(group_size), sdt))
     if nb == 0 or ns == 0:
         raise BitDeltaError(BD_ERR_CONFIG, "bd_prepare_tenant")
-    so = torch.empty(nb // 4, dtype=torch.int32, device=signs.device)
-    sc = torch.empty(ns // scales.element_size(), dtype=scales.dtype, device=signs.device)
+    so = _made_on(stream, torch.empty, nb // 4, dtype=torch.int32, device=signs.device)
+    sc = _made_on(stream, torch.empty, ns // scales.element_size(), dtype=scales.dtype, device=signs.device)
     rc = lib().bd_prepare_tenant(_ptr(signs), _ptr(scales), sdt, int(mode), int(group_size),
                                  int(d_out), int(d_in), _ptr(so), _ptr(sc), _stream(stream))
     check(rc, "bd_prepare_tenant")
@@ -378,10 +387,10 @@ def bd_apply_multi(w_base, table: TenantTable, tenant_ids, x, y=None, y_dtype=No
     d_out, d_in = w_base.shape
     batch = x.shape[0]
     if y is None:
-        y = torch.empty((batch, d_out), dtype=y_dtype or torch.bfloat16, device=x.device)
+        y = _made_on(stream, torch.empty, (batch, d_out), dtype=y_dtype or torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(max(bd_apply_workspace_size(d_out, d_in, batch, table.n), 16),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _made_on(stream, torch.empty, max(bd_apply_workspace_size(d_out, d_in, batch, table.n), 16),
+                             dtype=torch.uint8, device=x.device)
     rc = lib().bd_apply_multi(_ptr(w_base), dtype_code(w_base), d_out, d_in, table.ptr(), table.n,
                               table.scale_dtype, _ptr(tenant_ids), _ptr(x), batch, _ptr(y),
                               dtype_code(y), _ptr(workspace), workspace.numel(), _stream(stream))
@@ -395,9 +404,9 @@ def bd_quantize_base_fp8(w, codes=None, scales=None, stream=None):
     _require_cuda(w)
     d_out, d_in = w.shape
     if codes is None:
-        codes = torch.empty((d_out, d_in), dtype=torch.uint8, device=w.device)
+        codes = _made_on(stream, torch.empty, (d_out, d_in), dtype=torch.uint8, device=w.device)
     if scales is None:
-        scales = torch.empty(d_out, dtype=torch.float32, device=w.device)
+        scales = _made_on(stream, torch.empty, d_out, dtype=torch.float32, device=w.device)
     rc = lib().bd_quantize_base_fp8(_ptr(w), dtype_code(w), d_out, d_in, _ptr(codes), _ptr(scales), _stream(stream))
     check(rc, "bd_quantize_base_fp8")
     return codes, scales
@@ -416,10 +425,10 @@ def bd_apply_multi_fp8(w_codes, w_scales, table, tenant_ids, x, y=None, y_dtype=
     d_out, d_in = w_codes.shape
     batch = x.shape[0]
     if y is None:
-        y = torch.empty((batch, d_out), dtype=y_dtype or torch.bfloat16, device=x.device)
+        y = _made_on(stream, torch.empty, (batch, d_out), dtype=y_dtype or torch.bfloat16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(max(bd_apply_fp8_workspace_size(d_out, d_in, batch, table.n), 16),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _made_on(stream, torch.empty, max(bd_apply_fp8_workspace_size(d_out, d_in, batch, table.n), 16),
+                             dtype=torch.uint8, device=x.device)
     rc = lib().bd_apply_multi_fp8(_ptr(w_codes), _ptr(w_scales), d_out, d_in, table.ptr(), table.n,
                                   table.scale_dtype, _ptr(tenant_ids), _ptr(x), batch, _ptr(y), dtype_code(y),
                                   _ptr(workspace), workspace.numel(), _stream(stream))
@@ -485,15 +494,6 @@ def _fp4_call(name, dev, args, stream):
 
 def _p(t):
     return None if t is None else t.data_ptr()
-
-
-def _made_on(stream, make, *args):
-    """What a call allocates belongs to the stream that it launches on: fills come before its
-    kernels, and memory that is dropped goes to that stream's next allocation, not to another's."""
-    if stream is None:
-        return make(*args)
-    with (_FP4 or _fp4_env())["torch"].cuda.stream(stream):
-        return make(*args)
 
 
 def bd_fp4_scales_bytes(rows, cols, fmt) -> int:
