@@ -23,7 +23,11 @@
 // 180 us where the lookup kernel takes 225 (528 MB of signs and scales: floor 81). A call with
 // 32 ROW tenants and 256 tokens on 6144 x 4096 takes 95 us, with the lookup and fp16
 // tensor-core kernels 228. An item has 256 rows because a stage's barriers are paid per item
-// row block. Without effect or slower: a deeper ring of limbs, a stage's codes made before the
+// row block. A tenant's signs are expanded again for every 8 tokens, so its lead over the fp16
+// tensor-core kernel of the other bases (64 tokens of a tenant at a time) shrinks with the tokens
+// per tenant. 14336 x 4096, all of a call's delta kernels, this / fp16: 16 GROUP tenants with 16
+// tokens each 139 / 246 us, with 32 237 / 272; 4 with 64 138 / 123, with 128 237 / 192; ROW 130 / 247,
+// 214 / 273, 115 / 123, 194 / 192. Without effect or slower: a deeper ring of limbs, a stage's codes made before the
 // wait for its slot, a second MMA warp, two sets of sum warps, four banks of half the columns,
 // shifts on the multiplier.
 #include "bd_fp4_mma.cuh"

@@ -168,10 +168,19 @@ Fp4Plan plan_fp4(int64_t d_out, int64_t d_in, int64_t tokens, int limbs, int fmt
 bd_status launch_fp4_limbs(const Fp4Plan& p, int fmt, const void* x, int64_t d_in, int64_t tokens, uint8_t* xc,
                            uint8_t* xs, float* xmul, uint32_t* reset_status, cudaStream_t s);
 // The few-token kernel is bound by its unpacking, so its time grows with tokens * d_out * d_in;
-// the limbs and tensor-core kernels cost two launches. Measured on the device (us, few-token
-// kernel / the others, BD_FP4_NV): 1024 x 4096 1 token 3.0 / 6.1, 4 tokens 5.3 / 6.2;
-// 4096 x 4096 1 token 6.0 / 7.6, 2 tokens 7.5 / 7.7, 4 tokens 10.7 / 7.7; 4096 x 14336 1 token
-// 15.6 / 13.4; 28672 x 4096 1 token 27.7 / 15.9. The border is 2^25.
+// the limbs and tensor-core kernels cost two launches. Measured on the device, weights not in L2
+// (us, few-token kernel / the others):
+//                                NV            MX
+//   1024 x 4096   1 token     3.0 / 6.2     2.9 / 5.8
+//                 4 tokens    5.3 / 6.5     5.5 / 5.8
+//   2048 x 4096   4 tokens    8.3 / 7.5     8.6 / 6.6
+//   4096 x 4096   1 token     6.0 / 8.0     6.0 / 7.0
+//                 2 tokens    7.4 / 8.1     7.5 / 7.1
+//                 4 tokens   12.8 / 8.1    13.3 / 7.2
+//   4096 x 14336  1 token    16.2 / 14.4   16.9 / 12.8
+//   28672 x 4096  1 token    28.9 / 16.7   29.1 / 15.6
+// The border is 2^25 for both: what it loses next to it on the device is less than the second
+// launch costs the host, and the products are exact.
 constexpr int64_t kFp4GemvTokens = 4;
 inline bool fp4_use_gemv(int64_t d_out, int64_t d_in, int64_t tokens) {
   return tokens <= kFp4GemvTokens && tokens * d_out * d_in <= (1 << 25);
