@@ -95,12 +95,14 @@ __device__ __forceinline__ void load_group(uint32_t taddr, float* v) {
 }
 
 // v * a * b, the scales of a row and a token, without leaving fp32's range on the way to a result
-// inside it: the scales' product first, or one after the other where that is no normal number
-// (both are then large, or one is small and the other at most 2^23).
+// inside it: the scales' product first, or one after the other where that is no normal number. Then
+// both are large, or one is below 2^-63 (or zero) and the other any number that cannot make up for
+// it: the smaller one goes first where v is large or a scale is zero, else the larger one.
 __device__ __forceinline__ float scaled(float v, float a, float b) {
   const float q = a * b, m = fabsf(q);
   if (m >= 0x1p-126f && m <= 0x1.fffffep127f) return v * q;
-  return fabsf(a) > fabsf(b) ? v * a * b : v * b * a;
+  const bool smaller = fabsf(v) >= 0x1p60f || a == 0.f || b == 0.f;
+  return (fabsf(a) > fabsf(b)) != smaller ? v * a * b : v * b * a;
 }
 template <bool B>
 struct Flag {

@@ -143,6 +143,41 @@ def test_row_scales_of_tiny_blocks(bd, out, ew, ex, d_out, d_in, t):
     _check(y, ref, _bound(ref, w_hat, x_hat, 0 * x_hat, out))
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d_out,d_in,t", ENDS)
+def test_row_scales_of_zero(bd, fmt, d_out, d_in, t):
+    """A row or a token whose scale is zero gives zeros, whatever the other's scale."""
+    import torch
+    rng = np.random.default_rng(t)
+    w, wh = _packed(bd, rng, d_out, d_in, fmt)
+    x, xh = _packed(bd, rng, t, d_in, fmt)
+    for ew, ex in ((0, 122), (122, 0)):
+        wr, xr = _scaled(rng, d_out, ew), _scaled(rng, t, ex)
+        zero = wr if ex else xr
+        zero[::3] = 0
+        y, _ = bd.bd_matmul_fp4(w[0], w[1], dev(wr), x[0], x[1], dev(xr), fmt, y_dtype=torch.float32)
+        y = host(y) if ex else host(y).T
+        assert (y[:, ::3] == 0).all()
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("ew,ex", [(-140, 12), (12, -140), (-100, -45)])
+@pytest.mark.parametrize("d_out,d_in,t", ENDS)
+def test_row_scales_of_huge_blocks(bd, out, ew, ex, d_out, d_in, t):
+    """Sums near 2^120 that the larger scale would take past fp32's largest number before the
+    other, a subnormal, brings them back; two scales whose product is smaller than any number."""
+    rng = np.random.default_rng(d_in + t)
+    fmt = O.FP4_MX
+    c = [rng.integers(0, 256, size=(n, d_in // 2), dtype=np.uint8) for n in (d_out, t)]
+    s = [rng.integers(181, 184, size=(n, d_in // 32), dtype=np.uint8) for n in (d_out, t)]
+    wr, xr = (2.0 ** ew * np.ones(d_out)).astype(np.float32), (2.0 ** ex * np.ones(t)).astype(np.float32)
+    y, _ = bd.bd_matmul_fp4(dev(c[0]), dev(O.tile_scales(s[0])), dev(wr), dev(c[1]), dev(O.tile_scales(s[1])), dev(xr), fmt,
+                            y_dtype=_dtype(out))
+    w_hat, x_hat = O.dequantize_fp4(c[0], s[0], wr, fmt), O.dequantize_fp4(c[1], s[1], xr, fmt)
+    ref = x_hat @ w_hat.T
+    _check(y, ref, _bound(ref, w_hat, x_hat, 0 * x_hat, out))
+
+
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("t", [4, 5, 70])
 def test_linear_of_huge_weights_and_tiny_tokens(bd, out, t):
