@@ -502,8 +502,11 @@ def bd_fp4_scales_bytes(rows, cols, fmt) -> int:
 
 def fp4_scales_shape(rows, cols, fmt):
     """(row tiles, block tiles, 512): the tiled block scales of a [rows, cols] matrix."""
+    n = bd_fp4_scales_bytes(rows, cols, fmt)
+    if n == 0:
+        raise BitDeltaError(BD_ERR_SHAPE, "fp4_scales_shape")
     rt = -(-int(rows) // 128)
-    return (rt, bd_fp4_scales_bytes(rows, cols, fmt) // (512 * rt), 512)
+    return (rt, n // (512 * rt), 512)
 
 
 def fp4_buffers(rows, cols, fmt, device):
